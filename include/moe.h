@@ -415,6 +415,125 @@ MOE_API moe_status moe_forward_no_alloc(const moe_dims* dims,
                                         int E, int k, float capacity_factor,
                                         void* y, float* aux, int32_t* counts);
 
+/*
+ * The load-balance loss of a router with its per-expert counts, and the loss's
+ * gradient with respect to the router's logits: what training adds to the
+ * balance statistic that moe_forward returns (kevinluzbetak balancing list, "the
+ * gradient flows through P"; AI Engineering Illustrated "Mixture of Experts",
+ * "Fix 1", and DeepSeek-V3's loss per sequence). For each sequence s, over its
+ * n tokens that token_mask keeps:
+ *   p   = softmax(r)  (MOE_GATE_RENORM, MOE_GATE_RAW), or sigmoid(r) / sum
+ *         sigmoid(r) (MOE_GATE_SIGMOID); r is the logit the layer's softmax sees
+ *         (moe_workspace_layout_t.logits, plus the router bias if there is one)
+ *   c_i = entries of topk_idx equal to i over those tokens; f_i = c_i / (n k)
+ *   loss[s] = E sum_i f_i mean_t p_ti          (0 when n = 0)
+ *   dlogits[t, j] = dloss[s] (E / n) p_tj (f_j - sum_i f_i p_ti), and with
+ *         MOE_GATE_SIGMOID times 1 - sigmoid(r_tj)
+ * The counts carry no gradient. Entries of topk_idx outside [0, E) (a dropped or
+ * unrouted slot, -1) count for no expert; the same expert twice counts twice.
+ * Masked tokens, and tokens outside every sequence, count nowhere, whatever
+ * their logits hold, and get zero gradients. A row whose logits are all -inf has
+ * p = 0; NaN gives NaN (as does +inf under the softmax).
+ * Sums are fp32 over at most 1/148 of the batch, fp64 beyond, in a fixed order:
+ * the same inputs give the same bits. Limits: 1 <= k <= 32, k <= E <= 1024,
+ * T k < 2^31, num_seqs E < 2^31.
+ */
+typedef struct {
+  int64_t T;                 /* tokens (0 allowed) */
+  int32_t E, k;
+  int32_t dtype;             /* moe_dtype of logits and dlogits */
+  int32_t gate_mode;
+  int64_t ld;                /* elements from a row of logits to the next; 0 = E */
+  int32_t num_seqs;          /* S >= 1; 1 without cu_seqlens */
+  const int32_t* cu_seqlens; /* device [S + 1]: sequence s is tokens cu[s] .. cu[s + 1] - 1 (not
+                                decreasing; values outside 0..T are read as 0 or T); NULL =
+                                one sequence of all tokens */
+  const uint8_t* token_mask; /* device [T], nonzero = the token counts; NULL = all do */
+  void* workspace;           /* moe_balance_loss only: >= moe_balance_loss_workspace_size() bytes,
+                                256-byte aligned; needed until the call has run */
+  size_t workspace_bytes;
+  void* stream;
+} moe_balance_dims;
+
+MOE_API size_t moe_balance_loss_workspace_size(const moe_balance_dims* dims);
+
+/* logits device [T, E]; topk_idx device int32 [T, k]; written: loss fp32 [S],
+ * counts int32 [S, E], tokens int32 [S] (the n of each sequence). */
+MOE_API moe_status moe_balance_loss(const moe_balance_dims* dims, const void* logits,
+                                    const int32_t* topk_idx, float* loss, int32_t* counts,
+                                    int32_t* tokens);
+
+/* dloss device fp32 [S] (the gradient of each sequence's loss); counts and tokens
+ * as moe_balance_loss wrote them; dlogits device [T, E], dense, every row
+ * written. Needs no workspace and no topk_idx. */
+MOE_API moe_status moe_balance_loss_backward(const moe_balance_dims* dims, const float* dloss,
+                                             const void* logits, const int32_t* counts,
+                                             const int32_t* tokens, void* dlogits);
+
+/*
+ * E4M3 with one fp32 scale for each 128 along K (DeepSeek-V3's FP8 format:
+ * jacopoparretti "Mixture of experts, token by token", "Memory"): block_rows = 1
+ * scales each 1 x 128 piece of a row (activations), block_rows = 128 each
+ * 128 x 128 block (weights). scale = max(absmax / 448, 2^-126), 1 for an all-zero
+ * block; code = E4M3(w / scale), round to nearest even, saturating. A block with
+ * a NaN comes out as NaN; with an infinity, its scale is infinite.
+ *   w      device [stack, rows, cols], `dtype`; rows `ld` elements apart (0 =
+ *          cols; a multiple of 16 bytes), matrices rows * ld apart
+ *   codes  device uint8 [stack, rows, cols], dense
+ *   scales device fp32 [stack, ceil(rows / block_rows), ceil(cols / 128)]
+ * cols is a multiple of 16; edge blocks may be smaller than 128.
+ */
+MOE_API moe_status moe_quantize_fp8_block(const void* w, int32_t dtype, int64_t stack,
+                                          int64_t rows, int32_t cols, int64_t ld,
+                                          int32_t block_rows, uint8_t* codes, float* scales,
+                                          void* stream);
+
+/* out[..] = value(code) * scale of its block, rounded once to fp32 (device
+ * [stack, rows, cols]): the values the products below compute with. */
+MOE_API moe_status moe_dequantize_fp8_block(const uint8_t* codes, const float* scales,
+                                            int64_t stack, int64_t rows, int32_t cols,
+                                            int32_t block_rows, float* out, void* stream);
+
+/*
+ * Products on that format, dense or grouped by expert:
+ *   C[m, n] = sum_b sA[m, b] sW[n / 128, b] sum_{k in block b} A[m, k] W[n, k]
+ * in fp32, rounded once to the output type. Each K block is summed by the tensor
+ * cores, then added, times its scales, to fp32 accumulators.
+ * Grouped (E > 0): rows offsets[e] .. offsets[e + 1] - 1 meet expert e's matrix;
+ * any expert may have no rows, and rows before offsets[0] or behind offsets[E]
+ * are left as they were. Offsets are read on the device, without a host
+ * synchronisation; they must not decrease (values outside 0..M are read as 0 or
+ * M). Serving only: there is no gradient.
+ */
+typedef struct {
+  int64_t M;                /* rows of A (0 allowed: nothing is written) */
+  int32_t N, K;             /* W is [N, K]; K a multiple of 16 */
+  int32_t E;                /* experts (W [E, N, K], at most 1024); 0 = dense, W [N, K] */
+  int32_t out_dtype;        /* moe_matmul_fp8_block: MOE_BF16 or MOE_F32 */
+  int64_t lda;              /* bytes from a row of A to the next, a multiple of 16; 0 = K */
+  int64_t ld_out;           /* elements from a row of the output to the next; 0 = N */
+  const int32_t* offsets;   /* device [E + 1] when E > 0, else NULL */
+  const float* row_scale;   /* moe_matmul_fp8_block: device [M], factor of each output row (the
+                               layer's gates), or NULL */
+  uint64_t wait_timeout_ns; /* as in moe_dims */
+  void* stream;
+} moe_fp8_block_dims;
+
+/* a device uint8 [M, K] codes, a_scales fp32 [M, ceil(K / 128)] (block_rows = 1);
+ * w uint8 [E, N, K] codes, w_scales fp32 [E, ceil(N / 128), ceil(K / 128)]
+ * (block_rows = 128); out device [M, N]. */
+MOE_API moe_status moe_matmul_fp8_block(const moe_fp8_block_dims* dims, const uint8_t* a,
+                                        const float* a_scales, const uint8_t* w,
+                                        const float* w_scales, void* out);
+
+/* The first half of the experts in one kernel: H = SiLU(A W_g^T) * (A W_u^T) in
+ * fp32, then H quantised with block_rows = 1: codes uint8 [M, N] (N a multiple of
+ * 16) and scales fp32 [M, ceil(N / 128)], ready to be the next product's A. */
+MOE_API moe_status moe_swiglu_fp8_block(const moe_fp8_block_dims* dims, const uint8_t* a,
+                                        const float* a_scales, const uint8_t* W_g,
+                                        const uint8_t* W_u, const float* g_scales,
+                                        const float* u_scales, uint8_t* codes, float* scales);
+
 #ifdef __cplusplus
 }
 #endif

@@ -32,7 +32,9 @@ KERNEL_NAMES = ("router_logits", "route", "scan", "scatter", "gate_up_swiglu", "
 EXPORTED = ("moe_workspace_size", "moe_capacity", "moe_forward", "moe_forward_host_io",
             "moe_workspace_layout", "moe_get_device_status", "moe_status_string",
             "moe_forward_no_alloc", "moe_quantize_fp8", "moe_dequantize_fp8",
-            "moe_quantize_mxfp4", "moe_dequantize_mxfp4")
+            "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_balance_loss_workspace_size",
+            "moe_balance_loss", "moe_balance_loss_backward", "moe_quantize_fp8_block",
+            "moe_dequantize_fp8_block", "moe_matmul_fp8_block", "moe_swiglu_fp8_block")
 
 
 class moe_dims(ctypes.Structure):
@@ -75,6 +77,39 @@ class moe_workspace_layout_t(ctypes.Structure):
         ("hq", ctypes.c_size_t),
         ("hscale", ctypes.c_size_t),
         ("status", ctypes.c_size_t),
+    ]
+
+
+class moe_balance_dims(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int64),
+        ("E", ctypes.c_int32),
+        ("k", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("gate_mode", ctypes.c_int32),
+        ("ld", ctypes.c_int64),
+        ("num_seqs", ctypes.c_int32),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("token_mask", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class moe_fp8_block_dims(ctypes.Structure):
+    _fields_ = [
+        ("M", ctypes.c_int64),
+        ("N", ctypes.c_int32),
+        ("K", ctypes.c_int32),
+        ("E", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("lda", ctypes.c_int64),
+        ("ld_out", ctypes.c_int64),
+        ("offsets", ctypes.c_void_p),
+        ("row_scale", ctypes.c_void_p),
+        ("wait_timeout_ns", ctypes.c_uint64),
+        ("stream", ctypes.c_void_p),
     ]
 
 
@@ -137,6 +172,21 @@ def _open(path: str) -> ctypes.CDLL:
     lib.moe_quantize_mxfp4.restype = i32
     lib.moe_dequantize_mxfp4.argtypes = [vp, vp, vp, ctypes.c_int64, i32, vp, vp]
     lib.moe_dequantize_mxfp4.restype = i32
+    i64 = ctypes.c_int64
+    lib.moe_balance_loss_workspace_size.argtypes = [P(moe_balance_dims)]
+    lib.moe_balance_loss_workspace_size.restype = ctypes.c_size_t
+    lib.moe_balance_loss.argtypes = [P(moe_balance_dims), vp, vp, vp, vp, vp]
+    lib.moe_balance_loss.restype = i32
+    lib.moe_balance_loss_backward.argtypes = [P(moe_balance_dims), vp, vp, vp, vp, vp]
+    lib.moe_balance_loss_backward.restype = i32
+    lib.moe_quantize_fp8_block.argtypes = [vp, i32, i64, i64, i32, i64, i32, vp, vp, vp]
+    lib.moe_quantize_fp8_block.restype = i32
+    lib.moe_dequantize_fp8_block.argtypes = [vp, vp, i64, i64, i32, i32, vp, vp]
+    lib.moe_dequantize_fp8_block.restype = i32
+    lib.moe_matmul_fp8_block.argtypes = [P(moe_fp8_block_dims), vp, vp, vp, vp, vp]
+    lib.moe_matmul_fp8_block.restype = i32
+    lib.moe_swiglu_fp8_block.argtypes = [P(moe_fp8_block_dims), vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_swiglu_fp8_block.restype = i32
     return lib
 
 
@@ -258,3 +308,53 @@ def moe_dequantize_mxfp4(codes, block_scales, row_factors, rows: int, cols: int,
     return int(load().moe_dequantize_mxfp4(_ptr(codes) or None, _ptr(block_scales) or None,
                                            _ptr(row_factors) or None, int(rows), int(cols),
                                            _ptr(out) or None, int(stream) or None))
+
+
+def moe_balance_loss_workspace_size(dims) -> int:
+    return int(load().moe_balance_loss_workspace_size(_ref(dims)))
+
+
+def moe_balance_loss(dims, logits, topk_idx, loss, counts, tokens) -> int:
+    """Raw call: returns the status code."""
+    return int(load().moe_balance_loss(_ref(dims), _ptr(logits) or None, _ptr(topk_idx) or None,
+                                       _ptr(loss) or None, _ptr(counts) or None,
+                                       _ptr(tokens) or None))
+
+
+def moe_balance_loss_backward(dims, dloss, logits, counts, tokens, dlogits) -> int:
+    """Raw call: returns the status code."""
+    return int(load().moe_balance_loss_backward(_ref(dims), _ptr(dloss) or None,
+                                                _ptr(logits) or None, _ptr(counts) or None,
+                                                _ptr(tokens) or None, _ptr(dlogits) or None))
+
+
+def moe_quantize_fp8_block(w, dtype: int, stack: int, rows: int, cols: int, ld: int,
+                           block_rows: int, codes, scales, stream: int = 0) -> int:
+    """Raw call: returns the status code."""
+    return int(load().moe_quantize_fp8_block(_ptr(w) or None, int(dtype), int(stack), int(rows),
+                                             int(cols), int(ld), int(block_rows),
+                                             _ptr(codes) or None, _ptr(scales) or None,
+                                             int(stream) or None))
+
+
+def moe_dequantize_fp8_block(codes, scales, stack: int, rows: int, cols: int, block_rows: int, out,
+                             stream: int = 0) -> int:
+    """Raw call: returns the status code."""
+    return int(load().moe_dequantize_fp8_block(_ptr(codes) or None, _ptr(scales) or None, int(stack),
+                                               int(rows), int(cols), int(block_rows),
+                                               _ptr(out) or None, int(stream) or None))
+
+
+def moe_matmul_fp8_block(dims, a, a_scales, w, w_scales, out) -> int:
+    """Raw call: returns the status code."""
+    return int(load().moe_matmul_fp8_block(_ref(dims), _ptr(a) or None, _ptr(a_scales) or None,
+                                           _ptr(w) or None, _ptr(w_scales) or None,
+                                           _ptr(out) or None))
+
+
+def moe_swiglu_fp8_block(dims, a, a_scales, W_g, W_u, g_scales, u_scales, codes, scales) -> int:
+    """Raw call: returns the status code."""
+    return int(load().moe_swiglu_fp8_block(_ref(dims), _ptr(a) or None, _ptr(a_scales) or None,
+                                           _ptr(W_g) or None, _ptr(W_u) or None,
+                                           _ptr(g_scales) or None, _ptr(u_scales) or None,
+                                           _ptr(codes) or None, _ptr(scales) or None))

@@ -1,0 +1,346 @@
+// The load-balance loss of a router with its per-expert counts, and the loss's
+// gradient with respect to the logits, over a batch of ragged sequences.
+//
+// For each sequence s (the whole batch without cu_seqlens), over its n tokens
+// that the token mask keeps:
+//   p_t  = softmax(r_t)                       (RENORM, RAW)
+//        = sigmoid(r_t) / sum_j sigmoid(r_tj) (SIGMOID)
+//   c_i  = #{(t, slot): topk_idx = i},  f_i = c_i / (n k),  P_i = mean_t p_ti
+//   L    = E sum_i f_i P_i
+//   dL/dr_tj = (E / n) p_tj (f_j - sum_i f_i p_ti)   [SIGMOID: times 1 - sigmoid(r_tj)]
+// Sources: kevinluzbetak "Mixture-Of-Experts", balancing list (E sum f P, the
+// gradient flows through P alone: f is a count); AI Engineering Illustrated,
+// "Fix 1" and the sequence-level loss of DeepSeek-V3.
+//
+// Bound: memory. The forward pass reads the logits once, the gradient reads
+// them once more and writes as much (it needs f, a count over the whole
+// sequence). A row's softmax stays in the registers of one group of lanes.
+// Determinism: every sum has a fixed order (lane, then warp, then chunk);
+// counts are integers. The probability sums of a warp are fp32 over at most
+// one chunk of a sequence; everything above is fp64.
+#pragma once
+#include "common.cuh"
+#include "router.cuh"
+
+namespace moe {
+namespace bal {
+
+struct BalParams {
+  const void* logits;
+  int64_t ld;              // elements from a row of logits to the next
+  const int32_t* idx;      // [T, k]; entries outside [0, E) count for no expert
+  const uint8_t* mask;     // [T], nonzero = the token counts; NULL = all do
+  const int32_t* cu;       // [S + 1] first token of each sequence; NULL = one sequence
+  int T, E, k, S;
+  int chunk, nchunks;      // tokens per block of the forward kernel, and blocks
+  float* part_psum;        // [nchunks + S][E]: slot (chunk + sequence)
+  int32_t* part_counts;    // [nchunks + S][E]
+  int32_t* part_tokens;    // [nchunks + S]
+  float* loss;             // [S]
+  int32_t* counts;         // [S, E]
+  int32_t* tokens;         // [S]
+};
+
+// Sequence bounds, clamped so that any contents of cu stay inside the batch.
+__device__ __forceinline__ int seq_begin(const int32_t* cu, int s, int T) {
+  if (cu == nullptr) return 0;
+  const int v = cu[s];
+  return v < 0 ? 0 : (v > T ? T : v);
+}
+__device__ __forceinline__ int seq_end(const int32_t* cu, int s, int T) {
+  if (cu == nullptr) return T;
+  const int v = cu[s + 1], b = seq_begin(cu, s, T);
+  return v < b ? b : (v > T ? T : v);
+}
+// First sequence that ends behind token t (S when none does).
+__device__ __forceinline__ int first_seq_past(const int32_t* cu, int S, int t) {
+  if (cu == nullptr) return 0;
+  int lo = 0, hi = S;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid + 1] > t) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+template <int G> __device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+template <int G> __device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Probabilities of one row in place of its logits, and for SIGMOID the slope
+// 1 - sigmoid(r). Lane l of a group of G holds experts l, l + G, ... (NV of
+// them; those past E hold nothing). Both forms are scaled by the row's largest
+// term before the exponential, so that a row far below zero keeps its ratios;
+// sigmoid(r) = e^min(r,0) / (1 + e^-|r|). A row of only -inf has no
+// probabilities: all zero. NaN and +inf give NaN, as a softmax does.
+template <int G, int NV, bool SIG>
+__device__ __forceinline__ void row_probs(float* v, float* slope, int sub, int E) {
+  float m = -INFINITY;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (sub + G * i < E) {
+      m = fmaxf(m, v[i]);
+      nan |= v[i] != v[i];
+    }
+  m = group_max<G>(m);
+  if (SIG) m = fminf(m, 0.f);
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float z = 0.f;
+    if (sub + G * i < E && (m != -INFINITY || nan)) {
+      if (SIG) {
+        const float u = expf(-fabsf(v[i]));
+        const float r1 = __frcp_rn(1.f + u);
+        z = expf(fminf(v[i], 0.f) - m) * r1;
+        if (v[i] != v[i]) z = v[i];
+        slope[i] = v[i] >= 0.f ? u * r1 : r1;
+      } else {
+        z = expf(v[i] - m);
+      }
+    } else if (SIG) {
+      slope[i] = 0.f;
+    }
+    v[i] = z;
+    s += z;
+  }
+  s = group_sum<G>(s);
+  const float inv = s == 0.f ? 0.f : 1.f / s;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] *= inv;
+}
+
+// Deterministic block sum of a double (all threads get it); red holds 32.
+__device__ __forceinline__ double block_sum(double v, double* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[warp] = v;
+  __syncthreads();
+  double t = 0.0;
+  for (int w = 0; w < nw; ++w) t += red[w];
+  return t;
+}
+
+// L = E sum_i c_i psum_i / (n^2 k) from a block-wide sum of c_i psum_i.
+__device__ __forceinline__ float loss_of(double dot, int n, int E, int k) {
+  if (n == 0) return 0.f;
+  return (float)((double)E * dot / ((double)n * (double)n * (double)k));
+}
+
+// One block per chunk of tokens; warps take the chunk's tokens in turn, 32 / G
+// at a time. The block walks the sequences that its chunk meets; each leaves
+// its sums in slot (chunk + sequence), which no other pair has, or, when the
+// sequence lies inside the chunk, its results at once.
+// Dynamic shared memory: float psum[warps][E], int32 counts[E].
+template <typename TL, int G, int NV, bool SIG, int THREADS>
+__global__ void __launch_bounds__(THREADS) balance_kernel(const BalParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  extern __shared__ __align__(16) uint8_t bal_smem[];
+  constexpr int WARPS = THREADS / 32, PER = 32 / G;
+  float* s_psum = reinterpret_cast<float*>(bal_smem);
+  int32_t* s_cnt = reinterpret_cast<int32_t*>(s_psum + (size_t)WARPS * p.E);
+  __shared__ double s_red[32];
+  __shared__ int s_n;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane & (G - 1), grp = lane / G;
+  const TL* logits = static_cast<const TL*>(p.logits);
+  const int c0 = blockIdx.x * p.chunk;
+  const int c1 = min(p.T, c0 + p.chunk);
+  const bool alone = p.nchunks == 1;  // empty sequences are this block's too
+
+  for (int s = alone ? 0 : first_seq_past(p.cu, p.S, c0); s < p.S; ++s) {
+    const int qb = seq_begin(p.cu, s, p.T), qe = seq_end(p.cu, s, p.T);
+    if (!alone && qb >= c1) break;
+    const int b = max(qb, c0), e = min(qe, c1);
+    if (!alone && b >= e) continue;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.E; i += THREADS) s_cnt[i] = 0;
+    if (threadIdx.x == 0) s_n = 0;
+    __syncthreads();
+    float ps[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) ps[i] = 0.f;
+    int mine = 0;
+    for (int t0 = b + warp * PER; t0 < e; t0 += WARPS * PER) {
+      const int t = t0 + grp;
+      const bool live = t < e && (p.mask == nullptr || p.mask[t] != 0);
+      float v[NV], slope[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int x = sub + G * i;
+        v[i] = (live && x < p.E) ? to_f32(logits[(int64_t)t * p.ld + x]) : 0.f;
+      }
+      if (live)
+        for (int j = sub; j < p.k; j += G) {
+          const int x = p.idx[(int64_t)t * p.k + j];
+          if ((unsigned)x < (unsigned)p.E) atomicAdd(&s_cnt[x], 1);
+        }
+      row_probs<G, NV, SIG>(v, slope, sub, p.E);
+      if (live) {
+        mine += sub == 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) ps[i] += v[i];
+      }
+    }
+    // the groups of a warp hold the same experts: add them up
+#pragma unroll
+    for (int o = G; o < 32; o <<= 1) ps[0] += __shfl_xor_sync(0xffffffffu, ps[0], o);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (lane < G && sub + G * i < p.E) s_psum[(size_t)warp * p.E + sub + G * i] = ps[i];
+    if (mine) atomicAdd(&s_n, mine);
+    __syncthreads();
+    const bool whole = qb >= c0 && qe <= c1;
+    const size_t slot = (size_t)blockIdx.x + s;
+    const int n = s_n;
+    double dot = 0.0;
+    for (int i = threadIdx.x; i < p.E; i += THREADS) {
+      double acc = 0.0;
+      for (int w = 0; w < WARPS; ++w) acc += (double)s_psum[(size_t)w * p.E + i];
+      const int c = s_cnt[i];
+      if (whole) {
+        p.counts[(size_t)s * p.E + i] = c;
+        dot += (double)c * acc;
+      } else {
+        p.part_psum[slot * p.E + i] = (float)acc;
+        p.part_counts[slot * p.E + i] = c;
+      }
+    }
+    if (whole) {
+      dot = block_sum(dot, s_red);
+      if (threadIdx.x == 0) {
+        p.tokens[s] = n;
+        p.loss[s] = loss_of(dot, n, p.E, p.k);
+      }
+    } else if (threadIdx.x == 0) {
+      p.part_tokens[slot] = n;
+    }
+  }
+}
+
+// One block per sequence: those that met several chunks add their slots up,
+// empty ones get zeros. 32 experts at a time, 32 slots of each in parallel.
+__global__ void __launch_bounds__(1024) balance_finish_kernel(const BalParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  __shared__ double s_ps[32][33];
+  __shared__ int s_c[32][33];
+  __shared__ double s_red[32];
+  const int s = blockIdx.x;
+  const int qb = seq_begin(p.cu, s, p.T), qe = seq_end(p.cu, s, p.T);
+  const bool empty = qb >= qe;
+  const int f = empty ? 0 : qb / p.chunk, l = empty ? -1 : (qe - 1) / p.chunk;
+  if (!empty && f == l) return;  // finished where it was read
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  double dot = 0.0;
+  for (int e0 = 0; e0 < p.E; e0 += 32) {
+    const int e = e0 + lane;
+    double ps = 0.0;
+    int c = 0;
+    if (e < p.E)
+      for (int j = f + row; j <= l; j += 32) {
+        ps += (double)p.part_psum[((size_t)j + s) * p.E + e];
+        c += p.part_counts[((size_t)j + s) * p.E + e];
+      }
+    __syncthreads();
+    s_ps[row][lane] = ps;
+    s_c[row][lane] = c;
+    __syncthreads();
+    if (row == 0 && e < p.E) {
+      for (int w = 1; w < 32; ++w) {
+        ps += s_ps[w][lane];
+        c += s_c[w][lane];
+      }
+      p.counts[(size_t)s * p.E + e] = c;
+      dot += (double)c * ps;
+    }
+  }
+  int n = 0;
+  for (int j = f + (int)threadIdx.x; j <= l; j += blockDim.x) n += p.part_tokens[(size_t)j + s];
+  dot = block_sum(dot, s_red);
+  const int total = (int)block_sum((double)n, s_red);
+  if (threadIdx.x == 0) {
+    p.tokens[s] = total;
+    p.loss[s] = loss_of(dot, total, p.E, p.k);
+  }
+}
+
+// The gradient: each warp takes `run` consecutive tokens, 32 / G at a time.
+// f - 1/E stands for f: the p of a row add up to 1, so the difference is the
+// same, and (c E - n k) is an exact integer, so an f near 1/E does not cancel.
+// Rows that are masked or lie in no sequence get zeros, whatever they hold.
+template <typename TL, int G, int NV, bool SIG>
+__global__ void __launch_bounds__(256) balance_backward_kernel(const BalParams p, const float* dloss,
+                                                               TL* dlogits, int run) {
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int PER = 32 / G;
+  const int lane = threadIdx.x & 31, sub = lane & (G - 1), grp = lane / G;
+  const int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int64_t b64 = w * run;
+  if (b64 >= p.T) return;  // warp-uniform
+  const int b = (int)b64, e = min(p.T, b + run);
+  const TL* logits = static_cast<const TL*>(p.logits);
+  int s = first_seq_past(p.cu, p.S, min(b + grp, p.T - 1)), have = -1;
+  int qb = 0, qe = 0;
+  float f[NV], coef = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) f[i] = 0.f;
+  if (s < p.S) { qb = seq_begin(p.cu, s, p.T); qe = seq_end(p.cu, s, p.T); }
+  for (int t0 = b; t0 < e; t0 += PER) {
+    const int t = t0 + grp;
+    while (s < p.S && t >= qe) {
+      if (++s < p.S) { qb = seq_begin(p.cu, s, p.T); qe = seq_end(p.cu, s, p.T); }
+    }
+    const bool inside = t < e && s < p.S && t >= qb;
+    const bool live = inside && (p.mask == nullptr || p.mask[t] != 0);
+    float v[NV], slope[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int x = sub + G * i;
+      v[i] = (live && x < p.E) ? to_f32(logits[(int64_t)t * p.ld + x]) : 0.f;
+    }
+    if (live && have != s) {
+      have = s;
+      const int n = p.tokens[s];
+      const double nk = (double)n * (double)p.k;
+      coef = n > 0 ? (float)((double)dloss[s] * (double)p.E / (double)n) : 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int x = sub + G * i;
+        f[i] = (x < p.E && n > 0)
+                   ? (float)(((double)p.counts[(size_t)s * p.E + x] * (double)p.E - nk) /
+                             (nk * (double)p.E))
+                   : 0.f;
+      }
+    }
+    row_probs<G, NV, SIG>(v, slope, sub, p.E);
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) dot = fmaf(f[i], v[i], dot);
+    dot = group_sum<G>(dot);
+    if (t < e) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int x = sub + G * i;
+        float d = coef * v[i] * (f[i] - dot);
+        if (SIG) d *= slope[i];
+        if (x < p.E) dlogits[(int64_t)t * p.E + x] = from_f32<TL>(live ? d : 0.f);
+      }
+    }
+  }
+}
+
+}  // namespace bal
+}  // namespace moe

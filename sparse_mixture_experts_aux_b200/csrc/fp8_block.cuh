@@ -1,0 +1,207 @@
+// E4M3 with one fp32 scale for each block of 128 along K: pieces of 1 x 128 of
+// a row (activations) or blocks of 128 x 128 (weights).
+//   scale = max(absmax(block) / 448, 2^-126), 1 for an all-zero block
+//   code  = E4M3(x / scale), round to nearest even, saturating
+// (DeepSeek-V3's FP8 format; jacopoparretti "Mixture of experts, token by
+// token", "Memory".) A block that holds a NaN comes out as NaN; one that holds
+// an infinity has an infinite scale, finite elements 0 and infinite ones NaN.
+//
+// Bound: memory (bf16: 3 bytes an element, read and written once). The block
+// stays in registers between its maximum and its codes. The quotient is the
+// one of an fp32 division: q = x y corrected once by its remainder,
+// q + (x - q scale) y with y = 1 / scale (Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990), three fused
+// operations where a division of its own for each element would make these
+// kernels bound by arithmetic. Outside 2^-80 .. 2^100 the remainder could
+// underflow or the reciprocal vanish: such blocks divide.
+#pragma once
+#include "quant_formats.cuh"
+#include <float.h>
+
+namespace moe {
+namespace f8b {
+
+constexpr int BLK = 128;
+
+// NaN-propagating maximum of magnitudes.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float block_scale(float absmax) {
+  return absmax == 0.f ? 1.f : (absmax != absmax ? absmax : fmaxf(absmax / 448.0f, FLT_MIN));
+}
+
+struct Divisor {
+  float scale, inv;
+  bool fast;
+  __device__ __forceinline__ explicit Divisor(float s) : scale(s) {
+    fast = s > 0x1p-80f && s < 0x1p100f;
+    inv = fast ? __frcp_rn(s) : 0.f;
+  }
+  __device__ __forceinline__ float of(float x) const {
+    const float q = x * inv;
+    return fmaf(fmaf(-q, scale, x), inv, q);
+  }
+};
+
+// Two fp32 -> two E4M3 codes (a in the low byte), round to nearest even, saturating.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t encode4(const float* f, const Divisor& d) {
+  if (d.fast)
+    return e4m3x2(d.of(f[0]), d.of(f[1])) | e4m3x2(d.of(f[2]), d.of(f[3])) << 16;
+  return e4m3x2(__fdiv_rn(f[0], d.scale), __fdiv_rn(f[1], d.scale)) |
+         e4m3x2(__fdiv_rn(f[2], d.scale), __fdiv_rn(f[3], d.scale)) << 16;
+}
+
+// Sixteen consecutive elements held as raw 16-byte vectors.
+template <typename TX> struct Vec16E {
+  static constexpr int NVEC = 16 * sizeof(TX) / 16;
+  uint4 u[NVEC];
+  __device__ __forceinline__ void load(const TX* p) {
+#pragma unroll
+    for (int i = 0; i < NVEC; ++i) u[i] = ld_nc_v4(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < NVEC; ++i) u[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void values(int i, float* f) const { Vec16<TX>::unpack(u[i], f); }
+  __device__ __forceinline__ float absmax() const {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < NVEC; ++i) {
+      float f[Vec16<TX>::N];
+      values(i, f);
+#pragma unroll
+      for (int j = 0; j < Vec16<TX>::N; ++j) m = max_nan(m, fabsf(f[j]));
+    }
+    return m;
+  }
+  __device__ __forceinline__ uint4 codes(const Divisor& d) const {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < NVEC; ++i) {
+      float f[Vec16<TX>::N];
+      values(i, f);
+#pragma unroll
+      for (int j = 0; j < Vec16<TX>::N / 4; ++j)
+        w[i * (Vec16<TX>::N / 4) + j] = encode4(f + 4 * j, d);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// 1 x 128 blocks: eight lanes a block, sixteen elements a lane.
+template <typename TX>
+__global__ void __launch_bounds__(256) quantize_row_blocks_kernel(
+    const TX* __restrict__ x, int64_t rows, int cols, int64_t ld, uint8_t* __restrict__ codes,
+    float* __restrict__ scales) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int kb = (cols + BLK - 1) / BLK;
+  const int64_t units = rows * kb;  // blocks
+  const int sub = threadIdx.x & 7;
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 3);
+  // whole warps take part in the shuffles: the bound is rounded up to a warp's four blocks
+  for (int64_t u0 = (int64_t)blockIdx.x * (blockDim.x >> 3) + (threadIdx.x >> 5) * 4; u0 < units;
+       u0 += step) {
+    const int64_t u = u0 + ((threadIdx.x & 31) >> 3);
+    int64_t r;
+    int b;
+    if (units <= 0x7fffffff) {
+      r = (uint32_t)u / (uint32_t)kb;
+      b = (int)((uint32_t)u - (uint32_t)r * (uint32_t)kb);
+    } else {
+      r = u / kb;
+      b = (int)(u - r * kb);
+    }
+    const int c = b * BLK + sub * 16;
+    const bool in = u < units && c < cols;
+    Vec16E<TX> v;
+    if (in) v.load(x + r * ld + c); else v.zero();
+    float m = v.absmax();
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float s = block_scale(m);
+    if (in) st_v4(codes + r * cols + c, v.codes(Divisor(s)));
+    if (u < units && sub == 0) scales[u] = s;
+  }
+}
+
+// 128 x 128 blocks: one block of 256 threads each, 64 elements a thread.
+template <typename TX>
+__global__ void __launch_bounds__(256) quantize_square_blocks_kernel(
+    const TX* __restrict__ x, int64_t rows, int cols, int64_t ld, int nb, int kb,
+    uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  pdl_wait();
+  pdl_launch_dependents();
+  __shared__ float red[8];
+  const int64_t tile = blockIdx.x;
+  const int64_t e = tile / ((int64_t)nb * kb);
+  const int in_e = (int)(tile - e * nb * kb);
+  const int rb = in_e / kb, cb = in_e - rb * kb;
+  const int c = cb * BLK + (threadIdx.x & 7) * 16;
+  const TX* src = x + e * rows * ld;
+  uint8_t* dst = codes + e * rows * cols;
+  Vec16E<TX> v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = (int64_t)rb * BLK + i * 32 + (threadIdx.x >> 3);
+    if (r < rows && c < cols) v[i].load(src + r * ld + c); else v[i].zero();
+  }
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max_nan(m, v[i].absmax());
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+  m = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m = max_nan(m, red[w]);
+  const float s = block_scale(m);
+  const Divisor d(s);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = (int64_t)rb * BLK + i * 32 + (threadIdx.x >> 3);
+    if (r < rows && c < cols) st_v4(dst + r * cols + c, v[i].codes(d));
+  }
+  if (threadIdx.x == 0) scales[tile] = s;
+}
+
+// out = value(code) * scale of its block, rounded once to fp32. Sixteen codes a thread.
+__global__ void __launch_bounds__(256) dequantize_blocks_kernel(
+    const uint8_t* __restrict__ codes, const float* __restrict__ scales, int64_t stack,
+    int64_t rows, int cols, int block_rows, float* __restrict__ out) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int vpr = cols / 16, kb = (cols + BLK - 1) / BLK;
+  const int64_t nb = (rows + block_rows - 1) / block_rows, n = stack * rows * vpr;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t row = i / vpr, e = row / rows, r = row - e * rows;
+    const int c = (int)(i - row * vpr) * 16;
+    const float s = scales[(e * nb + r / block_rows) * kb + c / BLK];
+    const uint4 v = ld_nc_v4(codes + i * 16);
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+    float4* o = reinterpret_cast<float4*>(out + i * 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t lo, hi;
+      tcf8::e4m3x4_to_f16x4(in[j], lo, hi);
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+      o[j] = make_float4(a.x * s, a.y * s, b.x * s, b.y * s);
+    }
+  }
+}
+
+}  // namespace f8b
+}  // namespace moe

@@ -1,0 +1,567 @@
+// Products of E4M3 matrices with one fp32 scale for each 128 along K (rows of
+// A: 1 x 128; weights W: 128 x 128), dense or grouped by expert, sm_100a:
+//
+//   C[m, n] = sum_b sA[m, b] sW[n / 128, b] sum_{k in block b} A[m, k] W[n, k]
+//
+// The tensor cores sum one block of 128 (four tcgen05.mma kind::f8f6f4, fp32 in
+// TMEM); the epilogue warps then promote it: they read the 128 x 256 partial
+// sums from TMEM and add them, times sA sW, to fp32 accumulators in their
+// registers, while the tensor cores sum the next block into the other half of
+// TMEM. Rows are the M side, so that a thread owns one row: its scale is one
+// register, and a 128-column tile half has one weight scale.
+//
+// Two epilogues behind the last block:
+//   MATMUL  C times an optional factor per row, bf16 or fp32
+//   SWIGLU  the tile is 128 columns of the gate product and the matching 128 of
+//           the up product: H = SiLU(gate) * up, and the tile's 128 columns are
+//           one block of H, which leaves as E4M3 codes and a scale
+// Sources: jacopoparretti "Mixture of experts, token by token", "Memory"
+// (DeepSeek-V3 ships FP8 weights); Zero to Frontier 13.1, "The MoE layer" (the
+// SwiGLU expert) and "In PyTorch" (grouped products over the experts).
+//
+// Warp roles (384 threads): warp 0 TMA producer, warp 1 TMEM owner and MMA
+// issuer, warps 4..11 epilogue (warp w reads TMEM lanes 32 (w % 4)..+31, the
+// two warps of a quadrant take 64 columns of each half of the tile). The
+// epilogue threads hold 128 accumulators and two pieces of 32 partial sums, so
+// the first warpgroup hands registers to them (setmaxnreg): 4 x 32 x 56 +
+// 8 x 32 x 216 = 62464 of the 384 x 168 = 64512 at launch.
+//
+// Tiles of 128 rows never straddle two experts; rows of a tile behind its
+// expert's last row are computed from whatever lies there and not stored (a
+// row's sums depend on that row alone). A tile of few rows loads a smaller box
+// of A, and warps whose 32 rows are all behind the end skip their arithmetic.
+//
+// SPLIT (dense, few tiles): a cluster of S CTAs shares one tile, each sums a
+// range of K blocks, and the partial sums are added in rank order through
+// distributed shared memory (in the then idle operand ring): no workspace, no
+// atomics, the same bits every time.
+//
+// Every wait is bounded; see tc_gemm.cuh for the protocol.
+#pragma once
+#include "fp8_block.cuh"
+#include "tc2_gemm.cuh"
+
+namespace moe {
+namespace f8b {
+
+enum { MATMUL = 0, SWIGLU = 1 };
+
+constexpr int BM = 128, BN = 256;
+constexpr int A_BYTES = BM * BLK, B_BYTES = BN * BLK, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int STAGES = 4;
+constexpr int NUM_THREADS = 384, EPI_WARPS = 8, FIRST_EPI_WARP = 4;
+constexpr int CTRL_REGS = 56, EPI_REGS = 216;
+constexpr int A_BOXES = 3;  // tensor maps of A with boxes of 16, 64 and 128 rows
+constexpr int BAR_BYTES = 256;
+constexpr int SEG_BYTES = 4 * (3 * tc::MAX_E + 1);
+constexpr int MAX_BYTES = 2 * 2 * BM * 4;  // SWIGLU: row maxima of the two half tiles, double-buffered
+constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + BAR_BYTES + SEG_BYTES + MAX_BYTES;
+constexpr int DUMP_LD = BN + 4;  // floats a row of the split's partial sums (16-byte phases apart)
+static_assert(SMEM_BYTES <= 232448, "shared memory per block");
+static_assert(BM * DUMP_LD * 4 <= STAGES * STAGE_BYTES, "the partial sums fit the ring");
+static_assert(128 * CTRL_REGS + 256 * EPI_REGS <= NUM_THREADS * 168, "register split");
+
+struct Maps {
+  CUtensorMap a[A_BOXES];  // [M][K] codes, boxes of 128 bytes x 16, 64, 128 rows
+  CUtensorMap w0, w1;      // [E][N][K] codes, boxes of 128 bytes x 128 rows (SWIGLU: gate, up)
+};
+
+struct Params {
+  // rows of each expert: offsets [E + 1] (consecutive runs of rows), or the
+  // layer's segments (tile_start in 128-row tiles, counts, capacity); neither: dense
+  const int32_t* offsets;
+  const int32_t* tile_start;
+  const int32_t* counts;
+  int64_t cap;
+  int E, M, N;
+  int n_tiles, k_blocks, n_blocks;  // tiles along N, blocks of 128 along K and N
+  const float* a_scale;             // [M][k_blocks]
+  const float* w_scale0;            // [E][n_blocks][k_blocks]
+  const float* w_scale1;
+  const float* row_scale;           // MATMUL: factor per row, NULL = 1
+  void* out;                        // MATMUL: C; SWIGLU: codes of H
+  int64_t out_ld;                   // elements
+  int out_f32;                      // MATMUL
+  int out_vec;                      // rows of `out` are 16-byte aligned
+  float* out_scale;                 // SWIGLU: [M][n_blocks]
+  unsigned long long timeout_ns, drain_timeout_ns;
+  int* call_err;
+};
+
+__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// Wait for this thread's TMEM loads; the registers pass through, so that no use
+// of them can be scheduled before.
+__device__ __forceinline__ void wait_ld(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+// acc[0..31] += m * r[0..31], two at a time (fma.rn.f32x2: each half rounds as fmaf does).
+__device__ __forceinline__ void promote32(float* acc, const uint32_t* r, float m) {
+  uint64_t mm;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(mm) : "r"(__float_as_uint(m)));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    uint64_t a, t;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(acc[2 * i]), "f"(acc[2 * i + 1]));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(t) : "r"(r[2 * i]), "r"(r[2 * i + 1]));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(t), "l"(mm));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[2 * i]), "=f"(acc[2 * i + 1]) : "l"(a));
+  }
+}
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// The bounded wait of tc::wait_fast without its out-of-line call: the epilogue
+// warps wait with 128 accumulators in registers, which a call would spill.
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                            unsigned long long timeout_ns) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 1;; ++it) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    if ((it & 15u) == 1u) {
+      if (*abort_flag) return false;
+      if (static_cast<uint64_t>(clock64() - t0) > wait_cycles(timeout_ns)) {
+        atomicOr(&g_dev_error, DEVERR_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+
+struct Tile {
+  int e, nb, row0, valid;
+};
+// Tile order: expert by expert; within an expert the row tiles are fastest, so
+// CTAs running at the same time share weight tiles through L2.
+__device__ __forceinline__ Tile decode(long long tile, const Params& p, const int32_t* s_start,
+                                       const int32_t* s_len, const int32_t* s_mt) {
+  const long long q = tile / p.n_tiles;
+  int lo = 0, hi = p.E - 1;  // last expert whose first row tile is at or before q
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s_mt[mid] <= q) lo = mid; else hi = mid - 1;
+  }
+  const int me = s_mt[lo + 1] - s_mt[lo];
+  const long long in_e = tile - (long long)p.n_tiles * s_mt[lo];
+  const int mi = (int)(in_e % me);
+  Tile t;
+  t.e = lo;
+  t.nb = (int)(in_e / me);
+  t.row0 = s_start[lo] + mi * BM;
+  t.valid = min(BM, s_len[lo] - mi * BM);
+  return t;
+}
+
+// n consecutive outputs of one row (n <= 32) from column `col`.
+__device__ __forceinline__ void store32(const Params& p, int64_t row, int col, const float* v,
+                                        float f) {
+  if (col >= p.N) return;
+  if (p.out_f32) {
+    float* o = static_cast<float*>(p.out) + row * p.out_ld + col;
+    if (p.out_vec && col + 32 <= p.N) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        reinterpret_cast<float4*>(o)[i] =
+            make_float4(f * v[4 * i], f * v[4 * i + 1], f * v[4 * i + 2], f * v[4 * i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (col + i < p.N) o[i] = f * v[i];
+    }
+  } else {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + row * p.out_ld + col;
+    if (p.out_vec && col + 32 <= p.N) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = f * v[8 * i + j];
+        st_v4(o + 8 * i, Vec16<__nv_bfloat16>::pack(h));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (col + i < p.N) o[i] = __float2bfloat16_rn(f * v[i]);
+    }
+  }
+}
+
+template <int MODE, bool SPLIT>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = tc::smem_addr(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
+  // bars: full[STAGES], empty[STAGES], tfull[2], tempty[2], done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int32_t* s_start = reinterpret_cast<int32_t*>(smem + STAGES * STAGE_BYTES + BAR_BYTES);
+  int32_t* s_len = s_start + tc::MAX_E;
+  int32_t* s_mt = s_len + tc::MAX_E;
+  float* s_max = reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES + BAR_BYTES + SEG_BYTES);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t stage0 = tc::smem_addr(smem);
+  const uint32_t bar0 = tc::smem_addr(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
+  const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      tc::mbar_init(full_bar(s), 1);
+      tc::mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      tc::mbar_init(tfull_bar(a), 1);
+      tc::mbar_init(tempty_bar(a), EPI_WARPS);
+    }
+    tc::mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int b = 0; b < A_BOXES; ++b) tc::prefetch_map(&maps.a[b]);
+    tc::prefetch_map(&maps.w0);
+    if (MODE == SWIGLU) tc::prefetch_map(&maps.w1);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(tc::smem_addr(tmem_slot), 512);
+    tc::tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  // each expert's rows, clamped so that any contents of the arrays stay inside [0, M)
+  for (int e = threadIdx.x; e < p.E; e += NUM_THREADS) {
+    int64_t b = 0, t = p.M;
+    if (p.offsets != nullptr) {
+      b = p.offsets[e];
+      t = p.offsets[e + 1];
+    } else if (p.tile_start != nullptr) {
+      b = (int64_t)p.tile_start[e] * ROW_TILE;
+      const int64_t c = p.counts[e];
+      t = b + (p.cap >= 0 && c > p.cap ? p.cap : c);
+    }
+    b = b < 0 ? 0 : (b > p.M ? p.M : b);
+    t = t < b ? b : (t > p.M ? p.M : t);
+    s_start[e] = (int)b;
+    s_len[e] = (int)(t - b);
+  }
+  __syncthreads();
+  if (warp == 2) {  // exclusive scan of the row tiles
+    int run = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int v = e < p.E ? (s_len[e] + BM - 1) / BM : 0;
+      int incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+      }
+      if (e < p.E) s_mt[e] = run + incl - v;
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) s_mt[p.E] = run;
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const long long total = (long long)p.n_tiles * s_mt[p.E];
+  const unsigned long long tmo = p.timeout_ns, drain_tmo = p.drain_timeout_ns;
+  // SPLIT: one tile a cluster, this CTA's range of K blocks
+  uint32_t rank = 0, ranks = 1;
+  if (SPLIT) {
+    rank = tc2::cluster_ctarank();
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  }
+  const long long first = SPLIT ? blockIdx.x / ranks : blockIdx.x;
+  const long long step = SPLIT ? total : gridDim.x;
+  const int kb0 = SPLIT ? (int)((long long)p.k_blocks * rank / ranks) : 0;
+  const int kb1 = SPLIT ? (int)((long long)p.k_blocks * (rank + 1) / ranks) : p.k_blocks;
+
+  if (warp < FIRST_EPI_WARP) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CTRL_REGS));
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- producer
+      uint32_t issued = 0, last_par = 0, phase = 0;
+      int stage = 0;
+      bool ok = true;
+      for (long long tile = first; ok && tile < total; tile += step) {
+        const Tile t = decode(tile, p, s_start, s_len, s_mt);
+        const int box = t.valid <= 16 ? 0 : (t.valid <= 64 ? 1 : 2);
+        const uint32_t bytes = (box == 0 ? 16 : (box == 1 ? 64 : 128)) * BLK + B_BYTES;
+        const int n0 = MODE == SWIGLU ? t.nb * BLK : t.nb * BN;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!tc::wait_fast(empty_bar(stage), phase ^ 1u, abort_flag, tmo)) { ok = false; break; }
+          const uint32_t sa = stage0 + stage * STAGE_BYTES;
+          const uint32_t sb = sa + A_BYTES;
+          const uint32_t fb = full_bar(stage);
+          tc::mbar_expect_tx(fb, bytes);
+          // coordinates in 32-bit words along K
+          tc::tma_load_3d(sa, &maps.a[box], fb, kb * (BLK / 4), t.row0, 0);
+          tc::tma_load_3d(sb, &maps.w0, fb, kb * (BLK / 4), n0, t.e);
+          if (MODE == SWIGLU)
+            tc::tma_load_3d(sb + B_BYTES / 2, &maps.w1, fb, kb * (BLK / 4), n0, t.e);
+          else
+            tc::tma_load_3d(sb + B_BYTES / 2, &maps.w0, fb, kb * (BLK / 4), n0 + BLK, t.e);
+          issued |= 1u << stage;
+          last_par = (last_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (!ok)  // let every copy this thread issued land before the CTA exits
+        for (int s = 0; s < STAGES; ++s)
+          if ((issued >> s) & 1u)
+            tc::wait_drain(full_bar(s), (last_par >> s) & 1u, abort_flag, drain_tmo);
+    } else if (warp == 1 && lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      constexpr uint32_t IDESC = tc::make_idesc_e4m3(BM, BN);
+      int stage = 0;
+      uint32_t phase = 0, acc = 0, acc_phase = 0;
+      bool ok = true;
+      for (long long tile = first; ok && tile < total; tile += step) {
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!tc::wait_fast(tempty_bar(acc), acc_phase ^ 1u, abort_flag, tmo) ||
+              !tc::wait_fast(full_bar(stage), phase, abort_flag, tmo)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const uint32_t sa = stage0 + stage * STAGE_BYTES;
+          const uint64_t ad = tc::sw128_kmajor_desc(sa);
+          const uint64_t bd = tc::sw128_kmajor_desc(sa + A_BYTES);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // 32 codes = 32 bytes = +2 in the address field
+            tc::tc_mma_e4m3(tmem_base + acc * BN, ad + 2u * kk, bd + 2u * kk, IDESC,
+                            kk != 0 ? 1u : 0u);
+          tc::tc_commit(empty_bar(stage));
+          tc::tc_commit(tfull_bar(acc));
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          acc ^= 1u;
+          if (acc == 0u) acc_phase ^= 1u;
+        }
+      }
+      tc::tc_commit(done_bar);
+      tc::wait_drain(done_bar, 0u, abort_flag, drain_tmo);
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
+    const int quad = warp & 3, half = (warp - FIRST_EPI_WARP) >> 2;
+    const int r_in_tile = quad * 32 + lane;
+    uint32_t acc = 0, acc_phase = 0, par = 0;
+    bool ok = true;
+    for (long long tile = first; tile < total; tile += step) {
+      const Tile t = decode(tile, p, s_start, s_len, s_mt);
+      const bool row_ok = r_in_tile < t.valid;
+      const bool work = quad * 32 < t.valid;  // warp-uniform
+      const int64_t row = (int64_t)t.row0 + r_in_tile;
+      const int b0 = MODE == SWIGLU ? t.nb : 2 * t.nb;
+      const int b1 = MODE == SWIGLU ? t.nb : min(2 * t.nb + 1, p.n_blocks - 1);
+      const float* ws0 = p.w_scale0 + ((int64_t)t.e * p.n_blocks + b0) * p.k_blocks;
+      const float* ws1 =
+          (MODE == SWIGLU ? p.w_scale1 : p.w_scale0) + ((int64_t)t.e * p.n_blocks + b1) * p.k_blocks;
+      const float* as = p.a_scale + row * p.k_blocks;
+      float c[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) c[i] = 0.f;
+      // this row's scales four blocks ahead; the tile's weight scales 32 blocks
+      // at a time, one a lane
+      auto a_at = [&](int kb) { return row_ok && kb < kb1 ? __ldg(as + kb) : 0.f; };
+      auto w_at = [&](const float* w, int kb) { return kb < kb1 ? __ldg(w + kb) : 0.f; };
+      float q0 = a_at(kb0), q1 = a_at(kb0 + 1), q2 = a_at(kb0 + 2), q3 = a_at(kb0 + 3);
+      float w0 = w_at(ws0, kb0 + lane), w1 = w_at(ws1, kb0 + lane);
+      float w0n = w_at(ws0, kb0 + 32 + lane), w1n = w_at(ws1, kb0 + 32 + lane);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int j = (kb - kb0) & 31;
+        if (j == 0 && kb != kb0) {
+          w0 = w0n;
+          w1 = w1n;
+          w0n = w_at(ws0, kb + 32 + lane);
+          w1n = w_at(ws1, kb + 32 + lane);
+        }
+        const float m0 = q0 * __shfl_sync(0xffffffffu, w0, j);
+        const float m1 = q0 * __shfl_sync(0xffffffffu, w1, j);
+        q0 = q1; q1 = q2; q2 = q3; q3 = a_at(kb + 4);
+        ok = wait_inline(tfull_bar(acc), acc_phase, abort_flag, tmo);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (work) {
+          tc::tc_fence_after();
+          const uint32_t tb =
+              tmem_base + acc * BN + half * 64 + (static_cast<uint32_t>(quad * 32) << 16);
+          uint32_t r0[32], r1[32];
+          ld32(tb, r0);
+          wait_ld(r0);
+          ld32(tb + 32, r1);
+          promote32(c, r0, m0);
+          wait_ld(r1);
+          ld32(tb + 128, r0);
+          promote32(c + 32, r1, m0);
+          wait_ld(r0);
+          ld32(tb + 160, r1);
+          promote32(c + 64, r0, m1);
+          wait_ld(r1);
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(tempty_bar(acc));
+          promote32(c + 96, r1, m1);
+        } else if (lane == 0) {
+          tc::mbar_arrive(tempty_bar(acc));
+        }
+        acc ^= 1u;
+        if (acc == 0u) acc_phase ^= 1u;
+      }
+      if (!ok) break;
+      if (SPLIT) {
+        // leave the partial sums in the ring: its copies and MMAs are over
+        if (row_ok) {
+          float* d = reinterpret_cast<float*>(smem) + (size_t)r_in_tile * DUMP_LD + half * 64;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            reinterpret_cast<float4*>(d)[i] =
+                make_float4(c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]);
+            reinterpret_cast<float4*>(d + 128)[i] = make_float4(
+                c[64 + 4 * i], c[64 + 4 * i + 1], c[64 + 4 * i + 2], c[64 + 4 * i + 3]);
+          }
+        }
+      } else if (MODE == MATMUL) {
+        if (row_ok) {
+          const float f = p.row_scale != nullptr ? p.row_scale[row] : 1.f;
+          const int col = t.nb * BN + half * 64;
+          store32(p, row, col, c, f);
+          store32(p, row, col + 32, c + 32, f);
+          store32(p, row, col + 128, c + 64, f);
+          store32(p, row, col + 160, c + 96, f);
+        }
+      } else if (work) {
+        const int col = t.nb * BLK + half * 64;
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          c[i] = silu_f32(c[i]) * c[64 + i];
+          if (col + i < p.N) m = max_nan(m, fabsf(c[i]));
+        }
+        float* mx = s_max + par * 2 * BM;
+        mx[half * BM + r_in_tile] = m;
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+        m = max_nan(m, mx[(half ^ 1) * BM + r_in_tile]);
+        const float s = block_scale(m);
+        const Divisor d(s);
+        if (row_ok) {
+          uint8_t* o = static_cast<uint8_t*>(p.out) + row * p.out_ld + col;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (col + 16 * i < p.N)  // N is a multiple of 16
+              st_v4(o + 16 * i,
+                    make_uint4(encode4(c + 16 * i, d), encode4(c + 16 * i + 4, d),
+                               encode4(c + 16 * i + 8, d), encode4(c + 16 * i + 12, d)));
+          if (half == 0) p.out_scale[row * p.n_blocks + t.nb] = s;
+        }
+      }
+      par ^= 1u;
+    }
+    // a warp that gave up must not leave its partner waiting for its maxima
+    if (MODE == SWIGLU && !SPLIT && !ok)
+      asm volatile("bar.arrive %0, 64;" ::"r"(1 + quad) : "memory");
+  }
+
+  if (SPLIT) {
+    __syncthreads();
+    tc2::cluster_sync();  // every rank's partial sums are in its ring
+    if (warp >= FIRST_EPI_WARP && first < total && !*abort_flag) {
+      const Tile t = decode(first, p, s_start, s_len, s_mt);
+      const int w = warp - FIRST_EPI_WARP;
+      if (MODE == MATMUL) {
+        // a warp adds up 128 columns of one row, four a lane
+        for (int u = rank + ranks * w; u < 2 * t.valid; u += ranks * EPI_WARPS) {
+          const int r = u >> 1, col = (u & 1) * 128 + lane * 4;
+          const uint32_t at = stage0 + (r * DUMP_LD + col) * 4;
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+          for (uint32_t k = 0; k < ranks; ++k) {
+            const float4 x = ld_cluster_v4(tc2::mapa_shared(at, k));
+            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+          }
+          const int64_t row = (int64_t)t.row0 + r;
+          const float f = p.row_scale != nullptr ? p.row_scale[row] : 1.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int n = t.nb * BN + col + i;
+            if (n < p.N) {
+              if (p.out_f32) static_cast<float*>(p.out)[row * p.out_ld + n] = f * v[i];
+              else static_cast<__nv_bfloat16*>(p.out)[row * p.out_ld + n] = __float2bfloat16_rn(f * v[i]);
+            }
+          }
+        }
+      } else {
+        for (int r = rank + ranks * w; r < t.valid; r += ranks * EPI_WARPS) {
+          const uint32_t at = stage0 + (r * DUMP_LD + lane * 4) * 4;
+          float g[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+          for (uint32_t k = 0; k < ranks; ++k) {
+            const uint32_t a = tc2::mapa_shared(at, k);
+            const float4 x = ld_cluster_v4(a), y = ld_cluster_v4(a + 512);
+            g[0] += x.x; g[1] += x.y; g[2] += x.z; g[3] += x.w;
+            u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
+          }
+          const int col = t.nb * BLK + lane * 4;
+          float m = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            g[i] = silu_f32(g[i]) * u[i];
+            if (col < p.N) m = max_nan(m, fabsf(g[i]));
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const float s = block_scale(m);
+          const int64_t row = (int64_t)t.row0 + r;
+          if (col < p.N)
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + row * p.out_ld + col) =
+                encode4(g, Divisor(s));
+          if (lane == 0) p.out_scale[row * p.n_blocks + t.nb] = s;
+        }
+      }
+    }
+    tc2::cluster_sync();  // nobody reads this ring any more
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  tc::record_call_status(abort_flag, p.call_err);
+  if (warp == 1) {
+    __syncwarp();
+    tc::tmem_dealloc(tmem_base, 512);
+  }
+}
+
+}  // namespace f8b
+}  // namespace moe

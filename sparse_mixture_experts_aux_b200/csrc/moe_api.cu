@@ -18,6 +18,9 @@
 #include "router_tc.cuh"
 #include "tc_wq_swap.cuh"
 #include "tc_ws_gemm.cuh"
+#include "balance.cuh"
+#include "fp8_block.cuh"
+#include "fp8_block_gemm.cuh"
 
 namespace {
 
@@ -195,6 +198,13 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn g_encode = nullptr;
 
+template <int MODE, bool SPLIT>
+bool f8b_attr() {
+  return cudaFuncSetAttribute(moe::f8b::gemm_kernel<MODE, SPLIT>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              moe::f8b::SMEM_BYTES) == cudaSuccess;
+}
+
 template <int EPI, int AR, bool Q8 = false>
 bool tc_attr() {
   return cudaFuncSetAttribute(moe::tc::tc_grouped_gemm_kernel<EPI, AR, Q8>,
@@ -347,6 +357,9 @@ moe_status device_setup(int* num_sms, int* pair_clusters = nullptr) {
       return MOE_ERR_CUDA;
     if (cudaFuncSetAttribute(moe::rtc::router_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              moe::rtc::SMEM_LIMIT) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    if (!f8b_attr<moe::f8b::MATMUL, false>() || !f8b_attr<moe::f8b::MATMUL, true>() ||
+        !f8b_attr<moe::f8b::SWIGLU, false>() || !f8b_attr<moe::f8b::SWIGLU, true>())
       return MOE_ERR_CUDA;
     const int rs = static_cast<int>(moe::route_smem_bytes(moe::tc::MAX_E));
     if (cudaFuncSetAttribute(moe::route_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -987,6 +1000,214 @@ moe_status forward_impl(const moe_dims* dims, const void* x, const float* W_r, c
   return launched();
 }
 
+// ---------------------------------------------------------------------------
+// Balance loss (balance.cuh).
+// ---------------------------------------------------------------------------
+moe_status check_balance(const moe_balance_dims* d) {
+  if (d == nullptr || d->T < 0 || d->E < 1 || d->k < 1 || d->k > d->E || d->num_seqs < 1 ||
+      (d->dtype != MOE_F32 && d->dtype != MOE_BF16) || d->gate_mode < MOE_GATE_RENORM ||
+      d->gate_mode > MOE_GATE_SIGMOID || (d->ld != 0 && d->ld < d->E) ||
+      (d->cu_seqlens == nullptr && d->num_seqs != 1) ||
+      (d->cu_seqlens != nullptr && !aligned(d->cu_seqlens, 4)))
+    return MOE_ERR_INVALID_ARG;
+  if (d->E > moe::tc::MAX_E || d->k > 32 || d->T >= (int64_t(1) << 31) ||
+      d->T * d->k >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(d->num_seqs) * d->E >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// Tokens per block of the forward kernel: about one block per SM of a B200, at
+// least 32 tokens. Depends on T alone, so the workspace size does too.
+int balance_chunk(int64_t T) {
+  const int64_t c = (T + 147) / 148;
+  return static_cast<int>(c < 32 ? 32 : c);
+}
+size_t balance_slots(const moe_balance_dims* d) {
+  const int64_t ch = balance_chunk(d->T);
+  return static_cast<size_t>((d->T + ch - 1) / ch + d->num_seqs);
+}
+
+moe::bal::BalParams balance_params(const moe_balance_dims* d, const void* logits) {
+  moe::bal::BalParams p{};
+  p.logits = logits;
+  p.ld = d->ld != 0 ? d->ld : d->E;
+  p.mask = d->token_mask;
+  p.cu = d->cu_seqlens;
+  p.T = static_cast<int>(d->T);
+  p.E = d->E;
+  p.k = d->k;
+  p.S = d->num_seqs;
+  p.chunk = balance_chunk(d->T);
+  p.nchunks = static_cast<int>((d->T + p.chunk - 1) / p.chunk);
+  return p;
+}
+
+// Experts a row's group of lanes holds: groups of 8, 16 or 32 lanes, and above
+// 32 experts 2 to 32 of them a lane. FN is called with <group, per lane>.
+#define MOE_BAL_DISPATCH(E, FN)   \
+  do {                            \
+    if ((E) <= 8) FN(8, 1);       \
+    else if ((E) <= 16) FN(16, 1); \
+    else if ((E) <= 32) FN(32, 1); \
+    else if ((E) <= 64) FN(32, 2); \
+    else if ((E) <= 128) FN(32, 4); \
+    else if ((E) <= 256) FN(32, 8); \
+    else if ((E) <= 512) FN(32, 16); \
+    else FN(32, 32);              \
+  } while (0)
+
+template <typename TL, bool SIG>
+void launch_balance(const moe::bal::BalParams& p, cudaStream_t st) {
+  const unsigned grid = p.nchunks < 1 ? 1u : static_cast<unsigned>(p.nchunks);
+#define MOE_BAL_FWD(G, NV)                                                                  \
+  launch_pdl(moe::bal::balance_kernel<TL, G, NV, SIG, (NV > 8 ? 256 : 1024)>, grid,          \
+             (NV > 8 ? 256 : 1024),                                                          \
+             static_cast<size_t>(p.E) * 4 * ((NV > 8 ? 8 : 32) + 1), st, p)
+  MOE_BAL_DISPATCH(p.E, MOE_BAL_FWD);
+#undef MOE_BAL_FWD
+  if (p.nchunks > 1)
+    launch_pdl(moe::bal::balance_finish_kernel, static_cast<unsigned>(p.S), 1024, 0, st, p);
+}
+
+template <typename TL, bool SIG>
+void launch_balance_backward(const moe::bal::BalParams& p, const float* dloss, TL* dlogits,
+                             cudaStream_t st) {
+  // a warp's run of tokens: about 16 warps an SM, at least one round of its groups
+  const int per = p.E <= 8 ? 4 : (p.E <= 16 ? 2 : 1);
+  int64_t run = (static_cast<int64_t>(p.T) + 148 * 32 - 1) / (148 * 32);
+  run = (run + per - 1) / per * per;
+  const int64_t warps = (p.T + run - 1) / run;
+  const unsigned grid = static_cast<unsigned>((warps + 7) / 8);
+#define MOE_BAL_BWD(G, NV)                                                              \
+  launch_pdl(moe::bal::balance_backward_kernel<TL, G, NV, SIG>, grid, 256, 0, st, p, dloss, \
+             dlogits, static_cast<int>(run))
+  MOE_BAL_DISPATCH(p.E, MOE_BAL_BWD);
+#undef MOE_BAL_BWD
+}
+
+// ---------------------------------------------------------------------------
+// Block-scaled FP8 products (fp8_block_gemm.cuh).
+// ---------------------------------------------------------------------------
+
+// Tensor map over codes [outer][rows][cols] (cols a multiple of 16, rows `ld`
+// bytes apart), box {128 bytes, box_rows, 1}, 128-byte swizzle; described as
+// 32-bit words. Everything outside reads as zero.
+bool encode_map_codes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
+                      uint64_t outer, uint64_t ld, uint32_t box_rows) {
+  cuuint64_t dims[3] = {cols / 4, rows, outer};
+  cuuint64_t strides[2] = {ld, ld * rows};
+  cuuint32_t box[3] = {moe::f8b::BLK / 4, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One product: p holds the operands' scales, the segments and the outputs; K,
+// N, E and M are checked. w1 is the up projection of SWIGLU.
+template <int MODE>
+moe_status launch_f8b(moe::f8b::Params& p, int K, const void* a, int64_t lda, const void* w0,
+                      const void* w1, int num_sms, cudaStream_t st) {
+  using namespace moe::f8b;
+  p.k_blocks = (K + BLK - 1) / BLK;
+  p.n_blocks = (p.N + BLK - 1) / BLK;
+  p.n_tiles = MODE == SWIGLU ? p.n_blocks : (p.n_blocks + 1) / 2;
+  Maps maps;
+  memset(&maps, 0, sizeof(maps));
+  const uint32_t boxes[A_BOXES] = {16, 64, 128};
+  for (int i = 0; i < A_BOXES; ++i)
+    if (!encode_map_codes(&maps.a[i], a, K, p.M, 1, lda, boxes[i])) return MOE_ERR_CUDA;
+  if (!encode_map_codes(&maps.w0, w0, K, p.N, p.E, K, BLK)) return MOE_ERR_CUDA;
+  if (MODE == SWIGLU && !encode_map_codes(&maps.w1, w1, K, p.N, p.E, K, BLK)) return MOE_ERR_CUDA;
+  // dense products of few tiles: clusters that share a tile, of the largest
+  // size that one wave holds (at least two K blocks a CTA)
+  const bool dense = p.offsets == nullptr && p.tile_start == nullptr;
+  const int64_t tiles = static_cast<int64_t>(p.n_tiles) * ((p.M + BM - 1) / BM);
+  int split = 1;
+  if (dense)
+    while (split < 8 && tiles * (split + 1) <= num_sms && p.k_blocks >= 2 * (split + 1)) ++split;
+  if (split > 1) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
+    cfg.blockDim = dim3(NUM_THREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, gemm_kernel<MODE, true>, maps, p) != cudaSuccess)
+      return MOE_ERR_CUDA;
+  } else {
+    const int64_t grid = dense && tiles < num_sms ? tiles : num_sms;
+    launch_pdl(gemm_kernel<MODE, false>, static_cast<unsigned>(grid), NUM_THREADS, SMEM_BYTES, st,
+               maps, p);
+  }
+  return launched();
+}
+
+moe_status check_f8b(const moe_fp8_block_dims* d, bool swiglu) {
+  if (d == nullptr || d->M < 0 || d->N < 1 || d->K < 16 || d->E < 0 || d->K % 16 != 0 ||
+      (d->E > 0) != (d->offsets != nullptr) || !aligned(d->offsets, 4) ||
+      !aligned(d->row_scale, 4) || (d->lda != 0 && (d->lda < d->K || d->lda % 16 != 0)) ||
+      (d->ld_out != 0 && d->ld_out < d->N) ||
+      (d->out_dtype != MOE_F32 && d->out_dtype != MOE_BF16))
+    return MOE_ERR_INVALID_ARG;
+  if (swiglu && (d->N % 16 != 0 || d->ld_out % 16 != 0 || d->row_scale != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (d->E > moe::tc::MAX_E || d->M >= (int64_t(1) << 31) - 256 || d->N > (1 << 30) ||
+      d->lda >= (int64_t(1) << 39) ||
+      static_cast<int64_t>(d->K) * d->N >= (int64_t(1) << 39))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+template <int MODE>
+moe_status run_f8b(const moe_fp8_block_dims* d, const uint8_t* a, const float* a_scales,
+                   const uint8_t* w0, const uint8_t* w1, const float* s0, const float* s1,
+                   void* out, float* out_scale) {
+  const moe_status s = check_f8b(d, MODE == moe::f8b::SWIGLU);
+  if (s != MOE_OK) return s;
+  if (d->M == 0) return MOE_OK;
+  const bool two = MODE == moe::f8b::SWIGLU;
+  const size_t out_el = two ? 1 : (d->out_dtype == MOE_BF16 ? 2 : 4);
+  if (a == nullptr || a_scales == nullptr || w0 == nullptr || s0 == nullptr || out == nullptr ||
+      (two && (w1 == nullptr || s1 == nullptr || out_scale == nullptr)) || !aligned(a, 16) ||
+      !aligned(w0, 16) || !aligned(w1, 16) || !aligned(a_scales, 4) || !aligned(s0, 4) ||
+      !aligned(s1, 4) || !aligned(out, two ? 16 : out_el) || !aligned(out_scale, 4))
+    return MOE_ERR_INVALID_ARG;
+  int num_sms = 0;
+  const moe_status ds = device_setup(&num_sms);
+  if (ds != MOE_OK) return ds;
+  moe::f8b::Params p{};
+  p.offsets = d->offsets;
+  p.E = d->E > 0 ? d->E : 1;
+  p.M = static_cast<int>(d->M);
+  p.N = d->N;
+  p.cap = -1;
+  p.a_scale = a_scales;
+  p.w_scale0 = s0;
+  p.w_scale1 = s1;
+  p.row_scale = d->row_scale;
+  p.out = out;
+  p.out_ld = d->ld_out != 0 ? d->ld_out : d->N;
+  p.out_f32 = d->out_dtype == MOE_F32;
+  p.out_vec = aligned(out, 16) && (p.out_ld * static_cast<int64_t>(out_el)) % 16 == 0;
+  p.out_scale = out_scale;
+  p.timeout_ns = d->wait_timeout_ns != 0 ? static_cast<unsigned long long>(d->wait_timeout_ns)
+                                         : kWaitTimeoutNs;
+  p.drain_timeout_ns = kDrainTimeoutNs;
+  return launch_f8b<MODE>(p, d->K, a, d->lda != 0 ? d->lda : d->K, w0, w1, num_sms,
+                          static_cast<cudaStream_t>(d->stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -1179,6 +1400,141 @@ moe_status moe_forward_no_alloc(const moe_dims* dims, const void* x, const float
   d2.workspace_bytes = MOE_NO_ALLOC_WORKSPACE_BYTES;
   return forward_impl(&d2, x, W_r, W_g, W_u, W_d, W_shared, E, k, capacity_factor, y, aux,
                       counts);
+}
+
+size_t moe_balance_loss_workspace_size(const moe_balance_dims* dims) {
+  if (check_balance(dims) != MOE_OK) return 0;
+  return align_up(balance_slots(dims) * (static_cast<size_t>(dims->E) * 8 + 4), 256);
+}
+
+moe_status moe_balance_loss(const moe_balance_dims* dims, const void* logits,
+                            const int32_t* topk_idx, float* loss, int32_t* counts,
+                            int32_t* tokens) {
+  const moe_status s = check_balance(dims);
+  if (s != MOE_OK) return s;
+  const size_t el = dims->dtype == MOE_BF16 ? 2 : 4;
+  if (loss == nullptr || counts == nullptr || tokens == nullptr || !aligned(loss, 4) ||
+      !aligned(counts, 4) || !aligned(tokens, 4) ||
+      (dims->T > 0 && (logits == nullptr || topk_idx == nullptr || !aligned(logits, el) ||
+                       !aligned(topk_idx, 4))))
+    return MOE_ERR_INVALID_ARG;
+  if (dims->workspace == nullptr || !aligned(dims->workspace, 256) ||
+      dims->workspace_bytes < moe_balance_loss_workspace_size(dims))
+    return MOE_ERR_WORKSPACE;
+  moe::bal::BalParams p = balance_params(dims, logits);
+  const size_t cells = balance_slots(dims) * static_cast<size_t>(p.E);
+  p.idx = topk_idx;
+  p.part_psum = static_cast<float*>(dims->workspace);
+  p.part_counts = reinterpret_cast<int32_t*>(p.part_psum + cells);
+  p.part_tokens = p.part_counts + cells;
+  p.loss = loss;
+  p.counts = counts;
+  p.tokens = tokens;
+  if (p.nchunks == 0) p.nchunks = 1;  // no tokens: one block writes the zeros
+  cudaStream_t st = static_cast<cudaStream_t>(dims->stream);
+  const bool sig = dims->gate_mode == MOE_GATE_SIGMOID;
+  if (dims->dtype == MOE_BF16) {
+    if (sig) launch_balance<__nv_bfloat16, true>(p, st);
+    else launch_balance<__nv_bfloat16, false>(p, st);
+  } else {
+    if (sig) launch_balance<float, true>(p, st);
+    else launch_balance<float, false>(p, st);
+  }
+  return launched();
+}
+
+moe_status moe_balance_loss_backward(const moe_balance_dims* dims, const float* dloss,
+                                     const void* logits, const int32_t* counts,
+                                     const int32_t* tokens, void* dlogits) {
+  const moe_status s = check_balance(dims);
+  if (s != MOE_OK) return s;
+  if (dims->T == 0) return MOE_OK;
+  const size_t el = dims->dtype == MOE_BF16 ? 2 : 4;
+  if (dloss == nullptr || logits == nullptr || counts == nullptr || tokens == nullptr ||
+      dlogits == nullptr || !aligned(dloss, 4) || !aligned(logits, el) || !aligned(counts, 4) ||
+      !aligned(tokens, 4) || !aligned(dlogits, el))
+    return MOE_ERR_INVALID_ARG;
+  moe::bal::BalParams p = balance_params(dims, logits);
+  p.counts = const_cast<int32_t*>(counts);
+  p.tokens = const_cast<int32_t*>(tokens);
+  cudaStream_t st = static_cast<cudaStream_t>(dims->stream);
+  const bool sig = dims->gate_mode == MOE_GATE_SIGMOID;
+  if (dims->dtype == MOE_BF16) {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(dlogits);
+    if (sig) launch_balance_backward<__nv_bfloat16, true>(p, dloss, o, st);
+    else launch_balance_backward<__nv_bfloat16, false>(p, dloss, o, st);
+  } else {
+    float* o = static_cast<float*>(dlogits);
+    if (sig) launch_balance_backward<float, true>(p, dloss, o, st);
+    else launch_balance_backward<float, false>(p, dloss, o, st);
+  }
+  return launched();
+}
+
+moe_status moe_quantize_fp8_block(const void* w, int32_t dtype, int64_t stack, int64_t rows,
+                                  int32_t cols, int64_t ld, int32_t block_rows, uint8_t* codes,
+                                  float* scales, void* stream) {
+  if (w == nullptr || codes == nullptr || scales == nullptr || stack < 0 || rows < 0 || cols < 1 ||
+      cols % 16 != 0 || (dtype != MOE_BF16 && dtype != MOE_F32) ||
+      (block_rows != 1 && block_rows != moe::f8b::BLK) || !aligned(scales, 4) || !aligned(w, 16) ||
+      !aligned(codes, 16) || (ld != 0 && (ld < cols || ld % (dtype == MOE_BF16 ? 8 : 4) != 0)))
+    return MOE_ERR_INVALID_ARG;
+  if (stack == 0 || rows == 0) return MOE_OK;
+  if (ld == 0) ld = cols;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t kb = (cols + moe::f8b::BLK - 1) / moe::f8b::BLK;
+  if (block_rows == 1) {
+    const int64_t n = stack * rows;
+    const int64_t blocks = (n * kb + 31) / 32;
+    const unsigned grid = static_cast<unsigned>(blocks < 148 * 64 ? blocks : 148 * 64);
+    if (dtype == MOE_BF16)
+      launch_pdl(moe::f8b::quantize_row_blocks_kernel<__nv_bfloat16>, grid, 256, 0, st,
+                 static_cast<const __nv_bfloat16*>(w), n, cols, ld, codes, scales);
+    else
+      launch_pdl(moe::f8b::quantize_row_blocks_kernel<float>, grid, 256, 0, st,
+                 static_cast<const float*>(w), n, cols, ld, codes, scales);
+    return launched();
+  }
+  const int64_t nb = (rows + moe::f8b::BLK - 1) / moe::f8b::BLK;
+  if (nb >= (int64_t(1) << 31) || stack * nb * kb >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  const unsigned grid = static_cast<unsigned>(stack * nb * kb);
+  if (dtype == MOE_BF16)
+    launch_pdl(moe::f8b::quantize_square_blocks_kernel<__nv_bfloat16>, grid, 256, 0, st,
+               static_cast<const __nv_bfloat16*>(w), rows, cols, ld, static_cast<int>(nb),
+               static_cast<int>(kb), codes, scales);
+  else
+    launch_pdl(moe::f8b::quantize_square_blocks_kernel<float>, grid, 256, 0, st,
+               static_cast<const float*>(w), rows, cols, ld, static_cast<int>(nb),
+               static_cast<int>(kb), codes, scales);
+  return launched();
+}
+
+moe_status moe_dequantize_fp8_block(const uint8_t* codes, const float* scales, int64_t stack,
+                                    int64_t rows, int32_t cols, int32_t block_rows, float* out,
+                                    void* stream) {
+  if (codes == nullptr || scales == nullptr || out == nullptr || stack < 0 || rows < 0 ||
+      cols < 1 || cols % 16 != 0 || (block_rows != 1 && block_rows != moe::f8b::BLK) ||
+      !aligned(codes, 16) || !aligned(out, 16) || !aligned(scales, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (stack == 0 || rows == 0) return MOE_OK;
+  const int64_t blocks = (stack * rows * (cols / 16) + 255) / 256;
+  launch_pdl(moe::f8b::dequantize_blocks_kernel, static_cast<unsigned>(blocks < 16384 ? blocks : 16384),
+             256, 0, static_cast<cudaStream_t>(stream), codes, scales, stack, rows, cols, block_rows,
+             out);
+  return launched();
+}
+
+moe_status moe_matmul_fp8_block(const moe_fp8_block_dims* dims, const uint8_t* a,
+                                const float* a_scales, const uint8_t* w, const float* w_scales,
+                                void* out) {
+  return run_f8b<moe::f8b::MATMUL>(dims, a, a_scales, w, nullptr, w_scales, nullptr, out, nullptr);
+}
+
+moe_status moe_swiglu_fp8_block(const moe_fp8_block_dims* dims, const uint8_t* a,
+                                const float* a_scales, const uint8_t* W_g, const uint8_t* W_u,
+                                const float* g_scales, const float* u_scales, uint8_t* codes,
+                                float* scales) {
+  return run_f8b<moe::f8b::SWIGLU>(dims, a, a_scales, W_g, W_u, g_scales, u_scales, codes, scales);
 }
 
 }  // extern "C"
