@@ -20,11 +20,17 @@
 // SwiGLU expert) and "In PyTorch" (grouped products over the experts).
 //
 // Warp roles (384 threads): warp 0 TMA producer, warp 1 TMEM owner and MMA
-// issuer, warps 4..11 epilogue (warp w reads TMEM lanes 32 (w % 4)..+31, the
-// two warps of a quadrant take 64 columns of each half of the tile). The
+// issuer, warp 3 brings the scales and the tile's place, four K blocks at a time,
+// into a ring in shared memory, warps 4..11 epilogue (warp w reads TMEM lanes
+// 32 (w % 4)..+31, the two warps of a quadrant take 64 columns of each half of
+// the tile). The
 // epilogue threads hold 128 accumulators and two pieces of 32 partial sums, so
 // the first warpgroup hands registers to them (setmaxnreg): 4 x 32 x 56 +
-// 8 x 32 x 216 = 62464 of the 384 x 168 = 64512 at launch.
+// 8 x 32 x 224 = 64512, the 384 x 168 at launch.
+//
+// The epilogue warps touch no global memory inside the K loop: with their scales
+// loaded by themselves, the wait for a TMEM read also waited for those loads in
+// some builds and not in others (8192^2 x 4096: 1.2 to 2.1 PFLOP/s by chance).
 //
 // Tiles of 128 rows never straddle two experts; rows of a tile behind its
 // expert's last row are computed from whatever lies there and not stored (a
@@ -45,20 +51,30 @@ namespace moe {
 namespace f8b {
 
 enum { MATMUL = 0, SWIGLU = 1 };
-
 constexpr int BM = 128, BN = 256;
 constexpr int A_BYTES = BM * BLK, B_BYTES = BN * BLK, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int STAGES = 4;
+constexpr int RING_BYTES = STAGES * STAGE_BYTES;
 constexpr int NUM_THREADS = 384, EPI_WARPS = 8, FIRST_EPI_WARP = 4;
-constexpr int CTRL_REGS = 56, EPI_REGS = 216;
+constexpr int CTRL_REGS = 56, EPI_REGS = 224;
 constexpr int A_BOXES = 3;  // tensor maps of A with boxes of 16, 64 and 128 rows
 constexpr int BAR_BYTES = 256;
-constexpr int SEG_BYTES = 4 * (3 * tc::MAX_E + 1);
+constexpr int SEG_BYTES = 4 * (tc::MAX_E + 1);
+constexpr int GROUP = 4;         // K blocks whose scales travel together
+constexpr int SCALE_SLOTS = 4;   // groups in flight
+struct ScaleSlot {
+  float a[GROUP][BM];            // the rows' scales
+  float2 w[GROUP];               // the weight scales of the tile's two halves
+  int e, nb, row0, valid;        // the tile, in its first group
+};
 constexpr int MAX_BYTES = 2 * 2 * BM * 4;  // SWIGLU: row maxima of the two half tiles, double-buffered
-constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + BAR_BYTES + SEG_BYTES + MAX_BYTES;
+constexpr int STAGING_BYTES = EPI_WARPS * 2048;  // 32 rows of 64 output bytes a warp
+constexpr int SMEM_BYTES = 1024 + RING_BYTES + STAGING_BYTES + BAR_BYTES +
+                           SCALE_SLOTS * (int)sizeof(ScaleSlot) + SEG_BYTES + MAX_BYTES;
+static_assert(sizeof(ScaleSlot) % 16 == 0, "slots stay aligned");
 constexpr int DUMP_LD = BN + 4;  // floats a row of the split's partial sums (16-byte phases apart)
 static_assert(SMEM_BYTES <= 232448, "shared memory per block");
-static_assert(BM * DUMP_LD * 4 <= STAGES * STAGE_BYTES, "the partial sums fit the ring");
+static_assert(BM * DUMP_LD * 4 <= RING_BYTES, "the partial sums fit the ring");
 static_assert(128 * CTRL_REGS + 256 * EPI_REGS <= NUM_THREADS * 168, "register split");
 
 struct Maps {
@@ -114,18 +130,17 @@ __device__ __forceinline__ void wait_ld(uint32_t* r) {
                :
                : "memory");
 }
-// acc[0..31] += m * r[0..31], two at a time (fma.rn.f32x2: each half rounds as fmaf does).
-__device__ __forceinline__ void promote32(float* acc, const uint32_t* r, float m) {
-  uint64_t mm;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(mm) : "r"(__float_as_uint(m)));
+// The same registers' values from here on (behind a wait above).
+__device__ __forceinline__ void pass_regs(uint32_t* r) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    uint64_t a, t;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(acc[2 * i]), "f"(acc[2 * i + 1]));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(t) : "r"(r[2 * i]), "r"(r[2 * i + 1]));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(t), "l"(mm));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[2 * i]), "=f"(acc[2 * i + 1]) : "l"(a));
-  }
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+// acc[i] += m * r[i]. Single fused adds: packed pairs (fma.rn.f32x2) came with 30
+// to 110 register moves a block that differed from build to build, and were
+// slower in each (4736 x 4096 x 8192: 136 to 163 us, single ones 134).
+__device__ __forceinline__ void promote32(float* acc, const uint32_t* r, float m) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) acc[i] = fmaf(m, __uint_as_float(r[i]), acc[i]);
 }
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   float4 v;
@@ -136,80 +151,166 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   return v;
 }
 
-// The bounded wait of tc::wait_fast without its out-of-line call: the epilogue
-// warps wait with 128 accumulators in registers, which a call would spill.
+// Bounded wait for the phase with `parity` of barrier `bar`; false when another
+// role has given up or timeout_ns have passed (recorded, and the abort flag
+// raised). In line, unlike
+// the one in tc_gemm.cuh: the epilogue warps wait with 128 accumulators in
+// registers, which a call would spill. The first test does not suspend the warp and
+// the limit is checked before the next, so that a limit of nothing ends the
+// first wait that is not over.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
 __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                             unsigned long long timeout_ns) {
-  if (tc::mbar_try_wait(bar, parity)) return true;
+  if (mbar_test(bar, parity)) return true;
   const long long t0 = clock64();
-  for (uint32_t it = 1;; ++it) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
-    if ((it & 15u) == 1u) {
+  for (uint32_t it = 0;; ++it) {
+    if ((it & 15u) == 0u) {
       if (*abort_flag) return false;
-      if (static_cast<uint64_t>(clock64() - t0) > wait_cycles(timeout_ns)) {
+      if (static_cast<uint64_t>(clock64() - t0) >= wait_cycles(timeout_ns)) {
         atomicOr(&g_dev_error, DEVERR_TIMEOUT);
         *abort_flag = 1;
         return false;
       }
     }
+    if (tc::mbar_try_wait(bar, parity)) return true;
   }
 }
 
+// True in one lane of a converged warp. The issuing roles run with all lanes and
+// elect one for the copies and MMAs alone: issued from a branch on the lane
+// index, an MMA took 95 cycles to issue, and the issuer bounded the kernel.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0u;
+}
 struct Tile {
   int e, nb, row0, valid;
 };
+
+// First row and rows of expert e, clamped so that any contents of the arrays
+// stay inside [0, M).
+__device__ __forceinline__ void segment(const Params& p, int e, int* start, int* len) {
+  int64_t b = 0, t = p.M;
+  if (p.offsets != nullptr) {
+    b = p.offsets[e];
+    t = p.offsets[e + 1];
+  } else if (p.tile_start != nullptr) {
+    b = (int64_t)p.tile_start[e] * ROW_TILE;
+    const int64_t c = p.counts[e];
+    t = b + (p.cap >= 0 && c > p.cap ? p.cap : c);
+  }
+  b = b < 0 ? 0 : (b > p.M ? p.M : b);
+  t = t < b ? b : (t > p.M ? p.M : t);
+  *start = (int)b;
+  *len = (int)(t - b);
+}
+
 // Tile order: expert by expert; within an expert the row tiles are fastest, so
-// CTAs running at the same time share weight tiles through L2.
-__device__ __forceinline__ Tile decode(long long tile, const Params& p, const int32_t* s_start,
-                                       const int32_t* s_len, const int32_t* s_mt) {
-  const long long q = tile / p.n_tiles;
+// CTAs running at the same time share weight tiles through L2. s_mt: first row
+// tile of each expert.
+__device__ __forceinline__ Tile decode(int tile, const Params& p, const int32_t* s_mt) {
+  const int q = tile / p.n_tiles;
   int lo = 0, hi = p.E - 1;  // last expert whose first row tile is at or before q
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (s_mt[mid] <= q) lo = mid; else hi = mid - 1;
   }
   const int me = s_mt[lo + 1] - s_mt[lo];
-  const long long in_e = tile - (long long)p.n_tiles * s_mt[lo];
-  const int mi = (int)(in_e % me);
+  const int in_e = tile - p.n_tiles * s_mt[lo];
+  const int nb = in_e / me, mi = in_e - nb * me;
+  int start, len;
+  segment(p, lo, &start, &len);
   Tile t;
   t.e = lo;
-  t.nb = (int)(in_e / me);
-  t.row0 = s_start[lo] + mi * BM;
-  t.valid = min(BM, s_len[lo] - mi * BM);
+  t.nb = nb;
+  t.row0 = start + mi * BM;
+  t.valid = min(BM, len - mi * BM);
   return t;
 }
 
-// n consecutive outputs of one row (n <= 32) from column `col`.
-__device__ __forceinline__ void store32(const Params& p, int64_t row, int col, const float* v,
-                                        float f) {
-  if (col >= p.N) return;
-  if (p.out_f32) {
-    float* o = static_cast<float*>(p.out) + row * p.out_ld + col;
-    if (p.out_vec && col + 32 <= p.N) {
+// A warp's 32 rows of 64 output bytes, from registers (lane = row, four 16-byte
+// pieces) to global memory: through shared memory, so that a store instruction
+// writes 64 consecutive bytes of eight rows instead of 16 of 32. Piece c of row
+// r lies at c ^ (r / 2 % 4): conflict-free both ways. `rows` of the 32 and
+// `bytes` of the 64 exist; es = bytes of an element; vec: every row's first byte
+// is 16-byte aligned.
+__device__ __forceinline__ void store_rows64(uint8_t* stage, int lane, const uint4* v, uint8_t* out,
+                                             int64_t ld_bytes, int rows, int bytes, int es,
+                                             bool vec) {
+  __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        reinterpret_cast<float4*>(o)[i] =
-            make_float4(f * v[4 * i], f * v[4 * i + 1], f * v[4 * i + 2], f * v[4 * i + 3]);
-    } else {
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((c ^ (lane >> 1)) & 3) * 16) = v[c];
+  __syncwarp();
+  if (vec && (bytes & 15) == 0) {
+    const int c = lane & 3;
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col + i < p.N) o[i] = f * v[i];
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2);
+      if (r < rows && c * 16 < bytes)
+        *reinterpret_cast<uint4*>(out + r * ld_bytes + c * 16) =
+            *reinterpret_cast<const uint4*>(stage + r * 64 + ((c ^ (r >> 1)) & 3) * 16);
     }
   } else {
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + row * p.out_ld + col;
-    if (p.out_vec && col + 32 <= p.N) {
+    for (int r = 0; r < rows; ++r)
+      for (int b = lane * es; b < bytes; b += 32 * es) {
+        const uint8_t* from = stage + r * 64 + (((b >> 4) ^ (r >> 1)) & 3) * 16 + (b & 15);
+        if (es == 2)
+          *reinterpret_cast<uint16_t*>(out + r * ld_bytes + b) =
+              *reinterpret_cast<const uint16_t*>(from);
+        else
+          *reinterpret_cast<uint32_t*>(out + r * ld_bytes + b) =
+              *reinterpret_cast<const uint32_t*>(from);
+      }
+  }
+}
+
+// 32 columns of a warp's rows (lane = row; c: their sums) times the row's factor.
+__device__ __forceinline__ void store32(const Params& p, uint8_t* stage, int lane, int64_t row0,
+                                        int rows, int col, const float* c, float f) {
+  if (col >= p.N) return;
+  const int n = min(32, p.N - col);
+  if (p.out_f32) {
+    uint8_t* o = reinterpret_cast<uint8_t*>(static_cast<float*>(p.out) + row0 * p.out_ld + col);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float h[8];
+        float x[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = f * v[8 * i + j];
-        st_v4(o + 8 * i, Vec16<__nv_bfloat16>::pack(h));
+        for (int j = 0; j < 4; ++j) x[j] = f * c[16 * h + 4 * i + j];
+        v[i] = Vec16<float>::pack(x);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col + i < p.N) o[i] = __float2bfloat16_rn(f * v[i]);
+      if (n > 16 * h)
+        store_rows64(stage, lane, v, o + 64 * h, p.out_ld * 4, rows, 4 * min(16, n - 16 * h), 4,
+                     p.out_vec);
     }
+  } else {
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = f * c[8 * i + j];
+      v[i] = Vec16<__nv_bfloat16>::pack(x);
+    }
+    store_rows64(stage, lane, v,
+                 reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(p.out) + row0 * p.out_ld + col),
+                 p.out_ld * 2, rows, 2 * n, 2, p.out_vec);
   }
 }
 
@@ -219,16 +320,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = tc::smem_addr(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
-  // bars: full[STAGES], empty[STAGES], tfull[2], tempty[2], done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+  uint8_t* staging = smem + RING_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + STAGING_BYTES);
+  // bars: full[STAGES], empty[STAGES], tfull[2], tempty[2], done, sfull[SCALE_SLOTS],
+  // sempty[SCALE_SLOTS]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5 + 2 * SCALE_SLOTS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int32_t* s_start = reinterpret_cast<int32_t*>(smem + STAGES * STAGE_BYTES + BAR_BYTES);
-  int32_t* s_len = s_start + tc::MAX_E;
-  int32_t* s_mt = s_len + tc::MAX_E;
-  float* s_max = reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES + BAR_BYTES + SEG_BYTES);
+  ScaleSlot* slots = reinterpret_cast<ScaleSlot*>(staging + STAGING_BYTES + BAR_BYTES);
+  int32_t* s_mt = reinterpret_cast<int32_t*>(slots + SCALE_SLOTS);
+  float* s_max = reinterpret_cast<float*>(s_mt + tc::MAX_E + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // warp index as a warp-uniform value: what follows from it can live in uniform
+  // registers, which tcgen05.mma and the TMA copies take their operands from
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t stage0 = tc::smem_addr(smem);
   const uint32_t bar0 = tc::smem_addr(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -236,6 +340,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
   auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
   const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
+  auto sfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + s); };
+  auto sempty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + SCALE_SLOTS + s); };
+  uint32_t rank = 0, ranks = 1;  // SPLIT: in the cluster
+  if (SPLIT) {
+    rank = tc2::cluster_ctarank();
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -247,6 +358,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc::mbar_init(tempty_bar(a), EPI_WARPS);
     }
     tc::mbar_init(done_bar, 1);
+    for (int s = 0; s < SCALE_SLOTS; ++s) {
+      tc::mbar_init(sfull_bar(s), 1);
+      tc::mbar_init(sempty_bar(s), EPI_WARPS);
+    }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     for (int b = 0; b < A_BOXES; ++b) tc::prefetch_map(&maps.a[b]);
@@ -259,28 +374,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   pdl_wait();
   pdl_launch_dependents();
-  // each expert's rows, clamped so that any contents of the arrays stay inside [0, M)
-  for (int e = threadIdx.x; e < p.E; e += NUM_THREADS) {
-    int64_t b = 0, t = p.M;
-    if (p.offsets != nullptr) {
-      b = p.offsets[e];
-      t = p.offsets[e + 1];
-    } else if (p.tile_start != nullptr) {
-      b = (int64_t)p.tile_start[e] * ROW_TILE;
-      const int64_t c = p.counts[e];
-      t = b + (p.cap >= 0 && c > p.cap ? p.cap : c);
-    }
-    b = b < 0 ? 0 : (b > p.M ? p.M : b);
-    t = t < b ? b : (t > p.M ? p.M : t);
-    s_start[e] = (int)b;
-    s_len[e] = (int)(t - b);
-  }
-  __syncthreads();
-  if (warp == 2) {  // exclusive scan of the row tiles
+  if (warp == 2) {  // exclusive scan of the experts' row tiles
     int run = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
-      const int v = e < p.E ? (s_len[e] + BM - 1) / BM : 0;
+      int start, len = 0;
+      if (e < p.E) segment(p, e, &start, &len);
+      const int v = (len + BM - 1) / BM;
       int incl = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -296,153 +396,203 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const long long total = (long long)p.n_tiles * s_mt[p.E];
+  const int total = p.n_tiles * s_mt[p.E];  // the host bounds it below 2^31
   const unsigned long long tmo = p.timeout_ns, drain_tmo = p.drain_timeout_ns;
   // SPLIT: one tile a cluster, this CTA's range of K blocks
-  uint32_t rank = 0, ranks = 1;
-  if (SPLIT) {
-    rank = tc2::cluster_ctarank();
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
-  }
-  const long long first = SPLIT ? blockIdx.x / ranks : blockIdx.x;
-  const long long step = SPLIT ? total : gridDim.x;
+  const int first = blockIdx.x / ranks, step = SPLIT ? total : (int)gridDim.x;
   const int kb0 = SPLIT ? (int)((long long)p.k_blocks * rank / ranks) : 0;
   const int kb1 = SPLIT ? (int)((long long)p.k_blocks * (rank + 1) / ranks) : p.k_blocks;
+  auto wait_ctrl = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_inline(bar, parity, abort_flag, tmo)) != 0;
+  };
 
   if (warp < FIRST_EPI_WARP) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(CTRL_REGS));
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ---------------------------------------------------------- producer
       uint32_t issued = 0, last_par = 0, phase = 0;
       int stage = 0;
       bool ok = true;
-      for (long long tile = first; ok && tile < total; tile += step) {
-        const Tile t = decode(tile, p, s_start, s_len, s_mt);
+      for (int tile = first; ok && tile < total; tile += step) {
+        const Tile t = decode(tile, p, s_mt);
         const int box = t.valid <= 16 ? 0 : (t.valid <= 64 ? 1 : 2);
         const uint32_t bytes = (box == 0 ? 16 : (box == 1 ? 64 : 128)) * BLK + B_BYTES;
         const int n0 = MODE == SWIGLU ? t.nb * BLK : t.nb * BN;
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!tc::wait_fast(empty_bar(stage), phase ^ 1u, abort_flag, tmo)) { ok = false; break; }
+          ok = wait_ctrl(empty_bar(stage), phase ^ 1u);
+          if (!ok) break;
           const uint32_t sa = stage0 + stage * STAGE_BYTES;
           const uint32_t sb = sa + A_BYTES;
-          const uint32_t fb = full_bar(stage);
-          tc::mbar_expect_tx(fb, bytes);
-          // coordinates in 32-bit words along K
-          tc::tma_load_3d(sa, &maps.a[box], fb, kb * (BLK / 4), t.row0, 0);
-          tc::tma_load_3d(sb, &maps.w0, fb, kb * (BLK / 4), n0, t.e);
-          if (MODE == SWIGLU)
-            tc::tma_load_3d(sb + B_BYTES / 2, &maps.w1, fb, kb * (BLK / 4), n0, t.e);
-          else
-            tc::tma_load_3d(sb + B_BYTES / 2, &maps.w0, fb, kb * (BLK / 4), n0 + BLK, t.e);
+          const int x = kb * (BLK / 4);  // coordinates in 32-bit words along K
+          if (elect_one()) {
+            const uint32_t fb = full_bar(stage);
+            tc::mbar_expect_tx(fb, bytes);
+            tc::tma_load_3d(sa, &maps.a[box], fb, x, t.row0, 0);
+            tc::tma_load_3d(sb, &maps.w0, fb, x, n0, t.e);
+            tc::tma_load_3d(sb + B_BYTES / 2, MODE == SWIGLU ? &maps.w1 : &maps.w0, fb, x,
+                            MODE == SWIGLU ? n0 : n0 + BLK, t.e);
+          }
+          __syncwarp();
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
       }
-      if (!ok)  // let every copy this thread issued land before the CTA exits
+      if (!ok && lane == 0)  // let every copy of this warp land before the CTA exits
         for (int s = 0; s < STAGES; ++s)
           if ((issued >> s) & 1u)
             tc::wait_drain(full_bar(s), (last_par >> s) & 1u, abort_flag, drain_tmo);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer
       constexpr uint32_t IDESC = tc::make_idesc_e4m3(BM, BN);
       int stage = 0;
       uint32_t phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
-      for (long long tile = first; ok && tile < total; tile += step) {
+      for (int tile = first; ok && tile < total; tile += step) {
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!tc::wait_fast(tempty_bar(acc), acc_phase ^ 1u, abort_flag, tmo) ||
-              !tc::wait_fast(full_bar(stage), phase, abort_flag, tmo)) {
-            ok = false;
-            break;
-          }
+          ok = wait_ctrl(full_bar(stage), phase) && wait_ctrl(tempty_bar(acc), acc_phase ^ 1u);
+          if (!ok) break;
           tc::tc_fence_after();
           const uint32_t sa = stage0 + stage * STAGE_BYTES;
           const uint64_t ad = tc::sw128_kmajor_desc(sa);
           const uint64_t bd = tc::sw128_kmajor_desc(sa + A_BYTES);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // 32 codes = 32 bytes = +2 in the address field
-            tc::tc_mma_e4m3(tmem_base + acc * BN, ad + 2u * kk, bd + 2u * kk, IDESC,
-                            kk != 0 ? 1u : 0u);
-          tc::tc_commit(empty_bar(stage));
-          tc::tc_commit(tfull_bar(acc));
+            for (int kk = 0; kk < 4; ++kk)  // 32 codes = 32 bytes = +2 in the address field
+              tc::tc_mma_e4m3(tmem_base + acc * BN, ad + 2u * kk, bd + 2u * kk, IDESC,
+                              kk != 0 ? 1u : 0u);
+            tc::tc_commit(empty_bar(stage));
+            tc::tc_commit(tfull_bar(acc));
+          }
+          __syncwarp();
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
           acc ^= 1u;
           if (acc == 0u) acc_phase ^= 1u;
         }
       }
-      tc::tc_commit(done_bar);
-      tc::wait_drain(done_bar, 0u, abort_flag, drain_tmo);
+      if (elect_one()) {
+        tc::tc_commit(done_bar);
+        tc::wait_drain(done_bar, 0u, abort_flag, drain_tmo);
+      }
+      __syncwarp();
+    } else if (warp == 3) {
+      // ---------------------------------------------------------- scales
+      int slot = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = first; ok && tile < total; tile += step) {
+        const Tile t = decode(tile, p, s_mt);
+        const int b0 = MODE == SWIGLU ? t.nb : 2 * t.nb;
+        const int b1 = MODE == SWIGLU ? t.nb : min(2 * t.nb + 1, p.n_blocks - 1);
+        const float* w0 = p.w_scale0 + ((int64_t)t.e * p.n_blocks + b0) * p.k_blocks;
+        const float* w1 = (MODE == SWIGLU ? p.w_scale1 : p.w_scale0) +
+                          ((int64_t)t.e * p.n_blocks + b1) * p.k_blocks;
+        const float* as = p.a_scale + (int64_t)t.row0 * p.k_blocks;
+        for (int kb = kb0; kb < kb1; kb += GROUP) {
+          float v[4][GROUP], w = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < GROUP; ++k) {
+              const int r = 32 * i + lane;
+              v[i][k] = r < t.valid && kb + k < kb1 ? __ldg(as + (int64_t)r * p.k_blocks + kb + k)
+                                                    : 0.f;
+            }
+          if (lane < 2 * GROUP && kb + (lane >> 1) < kb1)
+            w = __ldg((lane & 1 ? w1 : w0) + kb + (lane >> 1));
+          ok = wait_ctrl(sempty_bar(slot), phase ^ 1u);
+          if (!ok) break;
+          ScaleSlot& s = slots[slot];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < GROUP; ++k) s.a[k][32 * i + lane] = v[i][k];
+          if (lane < 2 * GROUP) reinterpret_cast<float*>(s.w)[lane] = w;
+          if (lane == 0) {
+            s.e = t.e; s.nb = t.nb; s.row0 = t.row0; s.valid = t.valid;
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(sfull_bar(slot));
+          if (++slot == SCALE_SLOTS) { slot = 0; phase ^= 1u; }
+        }
+      }
     }
   } else {
     // ------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
     const int quad = warp & 3, half = (warp - FIRST_EPI_WARP) >> 2;
     const int r_in_tile = quad * 32 + lane;
-    uint32_t acc = 0, acc_phase = 0, par = 0;
-    bool ok = true;
-    for (long long tile = first; tile < total; tile += step) {
-      const Tile t = decode(tile, p, s_start, s_len, s_mt);
-      const bool row_ok = r_in_tile < t.valid;
-      const bool work = quad * 32 < t.valid;  // warp-uniform
-      const int64_t row = (int64_t)t.row0 + r_in_tile;
-      const int b0 = MODE == SWIGLU ? t.nb : 2 * t.nb;
-      const int b1 = MODE == SWIGLU ? t.nb : min(2 * t.nb + 1, p.n_blocks - 1);
-      const float* ws0 = p.w_scale0 + ((int64_t)t.e * p.n_blocks + b0) * p.k_blocks;
-      const float* ws1 =
-          (MODE == SWIGLU ? p.w_scale1 : p.w_scale0) + ((int64_t)t.e * p.n_blocks + b1) * p.k_blocks;
-      const float* as = p.a_scale + row * p.k_blocks;
+    uint8_t* stage = staging + (warp - FIRST_EPI_WARP) * 2048;
+    uint32_t acc = 0, acc_phase = 0, par = 0, sphase = 0;
+    int slot = 0;
+    bool ok = true, ready = false, sready = false;
+    for (int tile = first; tile < total; tile += step) {
       float c[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) c[i] = 0.f;
-      // this row's scales four blocks ahead; the tile's weight scales 32 blocks
-      // at a time, one a lane
-      auto a_at = [&](int kb) { return row_ok && kb < kb1 ? __ldg(as + kb) : 0.f; };
-      auto w_at = [&](const float* w, int kb) { return kb < kb1 ? __ldg(w + kb) : 0.f; };
-      float q0 = a_at(kb0), q1 = a_at(kb0 + 1), q2 = a_at(kb0 + 2), q3 = a_at(kb0 + 3);
-      float w0 = w_at(ws0, kb0 + lane), w1 = w_at(ws1, kb0 + lane);
-      float w0n = w_at(ws0, kb0 + 32 + lane), w1n = w_at(ws1, kb0 + 32 + lane);
+      Tile t{};
+      bool work = false;  // warp-uniform
       for (int kb = kb0; kb < kb1; ++kb) {
-        const int j = (kb - kb0) & 31;
-        if (j == 0 && kb != kb0) {
-          w0 = w0n;
-          w1 = w1n;
-          w0n = w_at(ws0, kb + 32 + lane);
-          w1n = w_at(ws1, kb + 32 + lane);
+        const int k = (kb - kb0) & (GROUP - 1);
+        // Both barriers of this block were tested before the last block's sums
+        // were added; only one that had not completed is waited for.
+        if (k == 0) {
+          if (!__all_sync(0xffffffffu, sready)) {
+            ok = wait_inline(sfull_bar(slot), sphase, abort_flag, tmo);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          if (kb == kb0) {
+            t.e = slots[slot].e; t.nb = slots[slot].nb;
+            t.row0 = slots[slot].row0; t.valid = slots[slot].valid;
+            work = quad * 32 < t.valid;
+          }
         }
-        const float m0 = q0 * __shfl_sync(0xffffffffu, w0, j);
-        const float m1 = q0 * __shfl_sync(0xffffffffu, w1, j);
-        q0 = q1; q1 = q2; q2 = q3; q3 = a_at(kb + 4);
-        ok = wait_inline(tfull_bar(acc), acc_phase, abort_flag, tmo);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        const float sa = slots[slot].a[k][r_in_tile];
+        const float2 sw = slots[slot].w[k];
+        if (!__all_sync(0xffffffffu, ready)) {
+          ok = wait_inline(tfull_bar(acc), acc_phase, abort_flag, tmo);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        const uint32_t tb =
+            tmem_base + acc * BN + half * 64 + (static_cast<uint32_t>(quad * 32) << 16);
+        uint32_t r0[32], r1[32];
         if (work) {
           tc::tc_fence_after();
-          const uint32_t tb =
-              tmem_base + acc * BN + half * 64 + (static_cast<uint32_t>(quad * 32) << 16);
-          uint32_t r0[32], r1[32];
+          // two loads in flight, each refilled as soon as its registers are free:
+          // a load takes about 160 cycles beside the MMAs' own TMEM traffic, and
+          // one at a time they were what bounded the kernel
           ld32(tb, r0);
-          wait_ld(r0);
           ld32(tb + 32, r1);
-          promote32(c, r0, m0);
-          wait_ld(r1);
-          ld32(tb + 128, r0);
-          promote32(c + 32, r1, m0);
           wait_ld(r0);
+          pass_regs(r1);
+          promote32(c, r0, sa * sw.x);
+          ld32(tb + 128, r0);
+          promote32(c + 32, r1, sa * sw.x);
           ld32(tb + 160, r1);
-          promote32(c + 64, r0, m1);
-          wait_ld(r1);
+          wait_ld(r0);
+          pass_regs(r1);
           tc::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(tempty_bar(acc));
-          promote32(c + 96, r1, m1);
-        } else if (lane == 0) {
-          tc::mbar_arrive(tempty_bar(acc));
         }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tempty_bar(acc));
         acc ^= 1u;
         if (acc == 0u) acc_phase ^= 1u;
+        if (k == GROUP - 1 || kb == kb1 - 1) {  // the group's scales have been read
+          if (lane == 0) tc::mbar_arrive(sempty_bar(slot));
+          if (++slot == SCALE_SLOTS) { slot = 0; sphase ^= 1u; }
+          sready = mbar_test(sfull_bar(slot), sphase);
+        }
+        ready = mbar_test(tfull_bar(acc), acc_phase);
+        if (work) {
+          promote32(c + 64, r0, sa * sw.y);
+          promote32(c + 96, r1, sa * sw.y);
+        }
       }
       if (!ok) break;
+      const bool row_ok = r_in_tile < t.valid;
+      const int64_t row = (int64_t)t.row0 + r_in_tile;
       if (SPLIT) {
         // leave the partial sums in the ring: its copies and MMAs are over
         if (row_ok) {
@@ -456,13 +606,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
       } else if (MODE == MATMUL) {
-        if (row_ok) {
-          const float f = p.row_scale != nullptr ? p.row_scale[row] : 1.f;
-          const int col = t.nb * BN + half * 64;
-          store32(p, row, col, c, f);
-          store32(p, row, col + 32, c + 32, f);
-          store32(p, row, col + 128, c + 64, f);
-          store32(p, row, col + 160, c + 96, f);
+        if (work) {
+          const float f = row_ok && p.row_scale != nullptr ? p.row_scale[row] : 1.f;
+          const int col = t.nb * BN + half * 64, rows = min(32, t.valid - quad * 32);
+          const int64_t r0 = (int64_t)t.row0 + quad * 32;
+          store32(p, stage, lane, r0, rows, col, c, f);
+          store32(p, stage, lane, r0, rows, col + 32, c + 32, f);
+          store32(p, stage, lane, r0, rows, col + 128, c + 64, f);
+          store32(p, stage, lane, r0, rows, col + 160, c + 96, f);
         }
       } else if (work) {
         const int col = t.nb * BLK + half * 64;
@@ -478,16 +629,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         m = max_nan(m, mx[(half ^ 1) * BM + r_in_tile]);
         const float s = block_scale(m);
         const Divisor d(s);
-        if (row_ok) {
-          uint8_t* o = static_cast<uint8_t*>(p.out) + row * p.out_ld + col;
+        uint4 v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (col + 16 * i < p.N)  // N is a multiple of 16
-              st_v4(o + 16 * i,
-                    make_uint4(encode4(c + 16 * i, d), encode4(c + 16 * i + 4, d),
-                               encode4(c + 16 * i + 8, d), encode4(c + 16 * i + 12, d)));
-          if (half == 0) p.out_scale[row * p.n_blocks + t.nb] = s;
-        }
+        for (int i = 0; i < 4; ++i)
+          v[i] = make_uint4(encode4(c + 16 * i, d), encode4(c + 16 * i + 4, d),
+                            encode4(c + 16 * i + 8, d), encode4(c + 16 * i + 12, d));
+        if (row_ok && half == 0) p.out_scale[row * p.n_blocks + t.nb] = s;
+        if (col < p.N)  // N is a multiple of 16
+          store_rows64(stage, lane, v,
+                       static_cast<uint8_t*>(p.out) + ((int64_t)t.row0 + quad * 32) * p.out_ld + col,
+                       p.out_ld, min(32, t.valid - quad * 32), min(64, p.N - col), 4, true);
       }
       par ^= 1u;
     }
@@ -500,7 +651,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncthreads();
     tc2::cluster_sync();  // every rank's partial sums are in its ring
     if (warp >= FIRST_EPI_WARP && first < total && !*abort_flag) {
-      const Tile t = decode(first, p, s_start, s_len, s_mt);
+      const Tile t = decode(first, p, s_mt);
       const int w = warp - FIRST_EPI_WARP;
       if (MODE == MATMUL) {
         // a warp adds up 128 columns of one row, four a lane

@@ -1114,6 +1114,9 @@ moe_status launch_f8b(moe::f8b::Params& p, int K, const void* a, int64_t lda, co
   p.k_blocks = (K + BLK - 1) / BLK;
   p.n_blocks = (p.N + BLK - 1) / BLK;
   p.n_tiles = MODE == SWIGLU ? p.n_blocks : (p.n_blocks + 1) / 2;
+  // the kernels count tiles in 32 bits
+  if ((static_cast<int64_t>(p.M) / BM + p.E + 1) * p.n_tiles >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
   Maps maps;
   memset(&maps, 0, sizeof(maps));
   const uint32_t boxes[A_BOXES] = {16, 64, 128};
@@ -1121,35 +1124,34 @@ moe_status launch_f8b(moe::f8b::Params& p, int K, const void* a, int64_t lda, co
     if (!encode_map_codes(&maps.a[i], a, K, p.M, 1, lda, boxes[i])) return MOE_ERR_CUDA;
   if (!encode_map_codes(&maps.w0, w0, K, p.N, p.E, K, BLK)) return MOE_ERR_CUDA;
   if (MODE == SWIGLU && !encode_map_codes(&maps.w1, w1, K, p.N, p.E, K, BLK)) return MOE_ERR_CUDA;
+  if (!encode_map_codes(&maps.w0, w0, K, p.N, p.E, K, BLK) ||
+      (MODE == SWIGLU && !encode_map_codes(&maps.w1, w1, K, p.N, p.E, K, BLK)))
+    return MOE_ERR_CUDA;
   // dense products of few tiles: clusters that share a tile, of the largest
   // size that one wave holds (at least two K blocks a CTA)
   const bool dense = p.offsets == nullptr && p.tile_start == nullptr;
   const int64_t tiles = static_cast<int64_t>(p.n_tiles) * ((p.M + BM - 1) / BM);
-  int split = 1;
+  int cluster = 1;
   if (dense)
-    while (split < 8 && tiles * (split + 1) <= num_sms && p.k_blocks >= 2 * (split + 1)) ++split;
-  if (split > 1) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
-    cfg.blockDim = dim3(NUM_THREADS);
-    cfg.dynamicSmemBytes = SMEM_BYTES;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, gemm_kernel<MODE, true>, maps, p) != cudaSuccess)
-      return MOE_ERR_CUDA;
-  } else {
-    const int64_t grid = dense && tiles < num_sms ? tiles : num_sms;
-    launch_pdl(gemm_kernel<MODE, false>, static_cast<unsigned>(grid), NUM_THREADS, SMEM_BYTES, st,
-               maps, p);
-  }
+    while (cluster < 8 && tiles * (cluster + 1) <= num_sms && p.k_blocks >= 2 * (cluster + 1))
+      ++cluster;
+  const int64_t grid = cluster > 1 || (dense && tiles < num_sms) ? tiles * cluster : num_sms;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  (void)(cluster > 1 ? cudaLaunchKernelEx(&cfg, gemm_kernel<MODE, true>, maps, p)
+                     : cudaLaunchKernelEx(&cfg, gemm_kernel<MODE, false>, maps, p));
   return launched();
 }
 

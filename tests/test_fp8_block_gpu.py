@@ -170,7 +170,8 @@ def near(got, want, mag, K, rows=slice(None)):
 @pytest.mark.parametrize("M,N,K", [
     (1, 1, 16), (1, 128, 128), (1, 4096, 7168), (2, 255, 144), (15, 257, 272), (16, 256, 1024),
     (17, 300, 1040), (33, 129, 400), (64, 512, 4096), (65, 1000, 512), (127, 77, 128), (128, 256, 128),
-    (129, 640, 2048), (200, 8, 4096), (1000, 333, 560), (8, 14336, 256)])
+    (129, 640, 2048), (200, 8, 4096), (1000, 333, 560), (8, 14336, 256),
+    (2500, 2100, 272), (6000, 1023, 144)])
 def test_dense(M, N, K, out_dtype):
     a, sa, w, sw = operands(M, N, K, 0, seed=M + N)
     c = matmul_fp8_block(a, sa, w, sw, out_dtype=out_dtype)
@@ -181,7 +182,9 @@ def test_dense(M, N, K, out_dtype):
 
 @pytest.mark.parametrize("lens,behind", [
     ([5], 0), ([0, 3, 0], 2), ([130, 1, 0, 127, 128, 129], 7), ([0, 0, 0], 4), ([1] * 40, 0),
-    ([16, 17, 64, 65, 300], 33), ([2, 0, 700, 0, 31], 1)])
+    ([16, 17, 64, 65, 300], 33), ([2, 0, 700, 0, 31], 1),
+    # several row tiles an expert, the last of them short
+    ([700, 400], 0), ([1, 129, 1900, 130], 9), ([0, 1537, 0], 3), ([640], 0), ([384, 1000, 256], 5)])
 @pytest.mark.parametrize("N,K", [(384, 512), (200, 272)])
 def test_grouped(lens, behind, N, K):
     E, M = len(lens), sum(lens) + behind
@@ -288,7 +291,7 @@ def check_swiglu(codes, scales, h, dh, rows=slice(None)):
 
 @pytest.mark.parametrize("M,N,K", [
     (1, 16, 16), (1, 1024, 4096), (2, 144, 272), (16, 128, 128), (31, 400, 1040), (64, 1024, 512),
-    (128, 256, 384), (129, 1040, 640), (500, 336, 256)])
+    (128, 256, 384), (129, 1040, 640), (500, 336, 256), (2500, 1040, 272)])
 def test_swiglu_dense(M, N, K):
     a, sa, g, sg = operands(M, N, K, 0, seed=N)
     _, _, u, su = operands(1, N, K, 0, seed=N + 50)
@@ -298,7 +301,8 @@ def test_swiglu_dense(M, N, K):
     assert moe_get_device_status() == 0
 
 
-@pytest.mark.parametrize("lens,behind", [([0, 3, 0, 130], 2), ([128, 1, 65, 16], 40), ([0, 0], 3)])
+@pytest.mark.parametrize("lens,behind", [([0, 3, 0, 130], 2), ([128, 1, 65, 16], 40), ([0, 0], 3),
+                                         ([700, 400], 0), ([1, 129, 1900, 130], 9), ([0, 1537, 0], 3)])
 def test_swiglu_grouped(lens, behind):
     E, M, N, K = len(lens), sum(lens) + behind, 272, 400
     offsets = [0]
@@ -388,12 +392,15 @@ def test_timeout_is_reported_and_the_context_stays_usable():
     want = matmul_fp8_block(a, sa, w, sw)
     torch.cuda.synchronize()
     assert moe_get_device_status() == 0
-    # clusters that share a tile (dense, few tiles) and single CTAs (grouped)
-    off = torch.tensor([0, 150, 200], dtype=torch.int32, device="cuda")
+    # single CTAs (grouped) and clusters that share a tile (dense)
     w2, sw2 = torch.stack([w, w]), torch.stack([sw, sw])
-    swiglu_fp8_block(a, sa, w2, w2, sw2, sw2, offsets=off, wait_timeout_ns=1)
-    torch.cuda.synchronize()
-    assert moe_get_device_status() == _lib.MOE_ERR_DEVICE_TIMEOUT
+    b, sb = a.repeat(6, 1), sa.repeat(6, 1)
+    for n in (200, 1200):
+        off = torch.tensor([0, n - 50, n], dtype=torch.int32, device="cuda")
+        swiglu_fp8_block(b[:n], sb[:n], w2, w2, sw2, sw2, offsets=off, wait_timeout_ns=1)
+        matmul_fp8_block(b[:n], sb[:n], w2, sw2, offsets=off, wait_timeout_ns=1)
+        torch.cuda.synchronize()
+        assert moe_get_device_status() == _lib.MOE_ERR_DEVICE_TIMEOUT
     for M in (1, 200):
         matmul_fp8_block(a[:M], sa[:M], w, sw, wait_timeout_ns=1)
         swiglu_fp8_block(a[:M], sa[:M], w, w, sw, sw, wait_timeout_ns=1)
