@@ -450,10 +450,13 @@ typedef struct {
                                 one sequence of all tokens */
   const uint8_t* token_mask; /* device [T], nonzero = the token counts; NULL = all do */
   void* workspace;           /* moe_balance_loss only: >= moe_balance_loss_workspace_size() bytes,
-                                256-byte aligned; needed until the call has run */
+                                256-byte aligned; needed until the call has run. Not used
+                                (may be NULL) for T <= MOE_BALANCE_SMALL_T tokens */
   size_t workspace_bytes;
   void* stream;
 } moe_balance_dims;
+
+#define MOE_BALANCE_SMALL_T 32 /* tokens that one thread block takes */
 
 MOE_API size_t moe_balance_loss_workspace_size(const moe_balance_dims* dims);
 

@@ -27,6 +27,7 @@ MOE_BF16 = 1
 MOE_GATE_RENORM, MOE_GATE_RAW, MOE_GATE_SIGMOID = 0, 1, 2
 MOE_WEIGHTS_DTYPE, MOE_WEIGHTS_FP8, MOE_WEIGHTS_FP8_W8A8, MOE_WEIGHTS_MXFP4 = 0, 1, 2, 3
 MOE_NUM_KERNELS = 7
+MOE_BALANCE_SMALL_T = 32
 KERNEL_NAMES = ("router_logits", "route", "scan", "scatter", "gate_up_swiglu", "down_scale", "combine")
 
 EXPORTED = ("moe_workspace_size", "moe_capacity", "moe_forward", "moe_forward_host_io",
@@ -316,45 +317,45 @@ def moe_balance_loss_workspace_size(dims) -> int:
 
 def moe_balance_loss(dims, logits, topk_idx, loss, counts, tokens) -> int:
     """Raw call: returns the status code."""
-    return int(load().moe_balance_loss(_ref(dims), _ptr(logits) or None, _ptr(topk_idx) or None,
-                                       _ptr(loss) or None, _ptr(counts) or None,
-                                       _ptr(tokens) or None))
+    return int(load().moe_balance_loss(_ref(dims), _ptr(logits), _ptr(topk_idx),
+                                       _ptr(loss), _ptr(counts),
+                                       _ptr(tokens)))
 
 
 def moe_balance_loss_backward(dims, dloss, logits, counts, tokens, dlogits) -> int:
     """Raw call: returns the status code."""
-    return int(load().moe_balance_loss_backward(_ref(dims), _ptr(dloss) or None,
-                                                _ptr(logits) or None, _ptr(counts) or None,
-                                                _ptr(tokens) or None, _ptr(dlogits) or None))
+    return int(load().moe_balance_loss_backward(_ref(dims), _ptr(dloss),
+                                                _ptr(logits), _ptr(counts),
+                                                _ptr(tokens), _ptr(dlogits)))
 
 
 def moe_quantize_fp8_block(w, dtype: int, stack: int, rows: int, cols: int, ld: int,
                            block_rows: int, codes, scales, stream: int = 0) -> int:
     """Raw call: returns the status code."""
-    return int(load().moe_quantize_fp8_block(_ptr(w) or None, int(dtype), int(stack), int(rows),
+    return int(load().moe_quantize_fp8_block(_ptr(w), int(dtype), int(stack), int(rows),
                                              int(cols), int(ld), int(block_rows),
-                                             _ptr(codes) or None, _ptr(scales) or None,
-                                             int(stream) or None))
+                                             _ptr(codes), _ptr(scales),
+                                             int(stream)))
 
 
 def moe_dequantize_fp8_block(codes, scales, stack: int, rows: int, cols: int, block_rows: int, out,
                              stream: int = 0) -> int:
     """Raw call: returns the status code."""
-    return int(load().moe_dequantize_fp8_block(_ptr(codes) or None, _ptr(scales) or None, int(stack),
+    return int(load().moe_dequantize_fp8_block(_ptr(codes), _ptr(scales), int(stack),
                                                int(rows), int(cols), int(block_rows),
-                                               _ptr(out) or None, int(stream) or None))
+                                               _ptr(out), int(stream)))
 
 
 def moe_matmul_fp8_block(dims, a, a_scales, w, w_scales, out) -> int:
     """Raw call: returns the status code."""
-    return int(load().moe_matmul_fp8_block(_ref(dims), _ptr(a) or None, _ptr(a_scales) or None,
-                                           _ptr(w) or None, _ptr(w_scales) or None,
-                                           _ptr(out) or None))
+    return int(load().moe_matmul_fp8_block(_ref(dims), _ptr(a), _ptr(a_scales),
+                                           _ptr(w), _ptr(w_scales),
+                                           _ptr(out)))
 
 
 def moe_swiglu_fp8_block(dims, a, a_scales, W_g, W_u, g_scales, u_scales, codes, scales) -> int:
     """Raw call: returns the status code."""
-    return int(load().moe_swiglu_fp8_block(_ref(dims), _ptr(a) or None, _ptr(a_scales) or None,
-                                           _ptr(W_g) or None, _ptr(W_u) or None,
-                                           _ptr(g_scales) or None, _ptr(u_scales) or None,
-                                           _ptr(codes) or None, _ptr(scales) or None))
+    return int(load().moe_swiglu_fp8_block(_ref(dims), _ptr(a), _ptr(a_scales),
+                                           _ptr(W_g), _ptr(W_u),
+                                           _ptr(g_scales), _ptr(u_scales),
+                                           _ptr(codes), _ptr(scales)))

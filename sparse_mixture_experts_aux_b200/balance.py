@@ -2,6 +2,7 @@
 argument checks and marshalling; the library computes."""
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import torch
@@ -14,8 +15,16 @@ from .layer import Workspace, dtype_code
 def _handle(stream, dev) -> int:
     """cudaStream_t to enqueue on: the device's current stream unless one is given."""
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev.index)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _on(dev):
+    """A context with `dev` current (the library launches on the current device)."""
+    return _HERE if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _lend(t: torch.Tensor, stream) -> None:
@@ -29,57 +38,60 @@ def _lend(t: torch.Tensor, stream) -> None:
 def _need(name: str, t: torch.Tensor, dtype, shape, dev) -> None:
     if t.device != dev:
         raise RuntimeError(f"{name} must be on {dev}, got {t.device}")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise RuntimeError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise RuntimeError(f"{name} must be contiguous")
 
 
-def _dims(logits, k, gate_mode, token_mask, cu_seqlens):
+def _args(logits, k, gate_mode, token_mask, cu_seqlens):
+    """Checks what both directions take; returns (T, E, S, fields of moe_balance_dims)."""
     if logits.dim() != 2:
         raise RuntimeError(f"logits must be [T, E], got {tuple(logits.shape)}")
     if not logits.is_cuda:
         raise RuntimeError("logits must be a CUDA tensor (there is no CPU path)")
     T, E = logits.shape
-    if E > 1 and logits.stride(1) != 1:
-        raise RuntimeError("logits must have their experts next to each other (stride 1)")
-    if T > 1 and logits.stride(0) < E:
-        raise RuntimeError("logits' rows must not overlap")
+    ld = E
+    if not logits.is_contiguous():
+        if E > 1 and logits.stride(1) != 1:
+            raise RuntimeError("logits must have their experts next to each other (stride 1)")
+        if T > 1:
+            ld = logits.stride(0)
+            if ld < E:
+                raise RuntimeError("logits' rows must not overlap")
     dev = logits.device
-    S = 1
+    S, cu, mask = 1, None, None
     if cu_seqlens is not None:
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise RuntimeError("cu_seqlens must be [S + 1] with S >= 1")
         S = cu_seqlens.numel() - 1
         _need("cu_seqlens", cu_seqlens, torch.int32, (S + 1,), dev)
+        cu = cu_seqlens.data_ptr()
     if token_mask is not None:
         _need("token_mask", token_mask, (torch.bool, torch.uint8), (T,), dev)
-    d = _lib.moe_balance_dims()
-    d.T, d.E, d.k, d.dtype = T, E, k, dtype_code(logits.dtype)
-    d.gate_mode, d.ld, d.num_seqs = int(gate_mode), logits.stride(0) if T > 1 else E, S
-    d.cu_seqlens = cu_seqlens.data_ptr() if cu_seqlens is not None else None
-    d.token_mask = token_mask.data_ptr() if token_mask is not None and T > 0 else None
-    return d
+        mask = token_mask.data_ptr() or None
+    return T, E, S, (T, E, k, dtype_code(logits.dtype), int(gate_mode), ld, S, cu, mask)
 
 
 def _forward(logits, topk_idx, gate_mode, token_mask, cu_seqlens, workspace, stream):
     if topk_idx.dim() != 2:
         raise RuntimeError(f"topk_idx must be [T, k], got {tuple(topk_idx.shape)}")
-    d = _dims(logits, topk_idx.shape[1], gate_mode, token_mask, cu_seqlens)
+    k = topk_idx.shape[1]
+    T, E, S, fields = _args(logits, k, gate_mode, token_mask, cu_seqlens)
     dev = logits.device
-    _need("topk_idx", topk_idx, torch.int32, (d.T, d.k), dev)
-    with torch.cuda.device(dev):
-        need = _lib.moe_balance_loss_workspace_size(d)
-        if need:  # a layer that is refused has no size: the call below says why
+    _need("topk_idx", topk_idx, torch.int32, (T, k), dev)
+    with _on(dev):
+        d = _lib.moe_balance_dims(*fields, None, 0, _handle(stream, dev))
+        need = _lib.moe_balance_loss_workspace_size(d) if T > _lib.MOE_BALANCE_SMALL_T else 0
+        if need:  # a call that is refused has no size: it says why below
             ws = (workspace or Workspace()).get(need, dev)
             d.workspace, d.workspace_bytes = ws.data_ptr(), ws.numel()
             _lend(ws, stream)
-        d.stream = _handle(stream, dev) or None
-        loss = torch.empty(d.num_seqs, dtype=torch.float32, device=dev)
-        counts = torch.empty(d.num_seqs, d.E, dtype=torch.int32, device=dev)
-        tokens = torch.empty(d.num_seqs, dtype=torch.int32, device=dev)
+        loss = torch.empty(S, dtype=torch.float32, device=dev)
+        counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+        tokens = torch.empty(S, dtype=torch.int32, device=dev)
         for t in (loss, counts, tokens):
             _lend(t, stream)
         rc = _lib.moe_balance_loss(d, logits, topk_idx, loss, counts, tokens)
@@ -97,16 +109,16 @@ def balance_loss_backward(dloss: torch.Tensor, logits: torch.Tensor, counts: tor
     dloss fp32 [S]: the gradient of each sequence's loss; counts and tokens as
     balance_loss returned them; k = topk_idx.shape[1]; the rest as there. This is
     the call behind balance_loss's autograd, for programs that chain gradients
-    themselves (it reads no autograd state, so it can be captured in a graph).
+    themselves (it touches no autograd state, so it can be captured in a graph).
     """
-    d = _dims(logits, int(k), gate_mode, token_mask, cu_seqlens)
+    T, E, S, fields = _args(logits, int(k), gate_mode, token_mask, cu_seqlens)
     dev = logits.device
-    _need("dloss", dloss, torch.float32, (d.num_seqs,), dev)
-    _need("counts", counts, torch.int32, (d.num_seqs, d.E), dev)
-    _need("tokens", tokens, torch.int32, (d.num_seqs,), dev)
-    with torch.cuda.device(dev):
-        d.stream = _handle(stream, dev) or None
-        dlogits = torch.empty(d.T, d.E, dtype=logits.dtype, device=dev)
+    _need("dloss", dloss, torch.float32, (S,), dev)
+    _need("counts", counts, torch.int32, (S, E), dev)
+    _need("tokens", tokens, torch.int32, (S,), dev)
+    with _on(dev):
+        d = _lib.moe_balance_dims(*fields, None, 0, _handle(stream, dev))
+        dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
         _lend(dlogits, stream)
         rc = _lib.moe_balance_loss_backward(d, dloss, logits, counts, tokens, dlogits)
     if rc != _lib.MOE_OK:

@@ -74,48 +74,80 @@ template <int G> __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// Probabilities of one row in place of its logits, and for SIGMOID the slope
-// 1 - sigmoid(r). Lane l of a group of G holds experts l, l + G, ... (NV of
-// them; those past E hold nothing). Both forms are scaled by the row's largest
-// term before the exponential, so that a row far below zero keeps its ratios;
-// sigmoid(r) = e^min(r,0) / (1 + e^-|r|). A row of only -inf has no
-// probabilities: all zero. NaN and +inf give NaN, as a softmax does.
+// 2^x and 1/x by the hardware: off by 2 ulp and 1 ulp, results below 2^-126 are
+// zero. With the library's expf and a true division, and a test of every
+// expert's index, a row of 256 took 540 instructions forward and 740 backward
+// and these kernels were bound by issuing them: 34 and 40 us for 32768 rows.
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// The terms of one row's probabilities in place of its logits; returns the
+// factor that makes them probabilities. SIGMOID: also the slope 1 - sigmoid(r).
+// Lane l of a group of G holds experts l, l + G, ... (NV of them; those past E
+// hold -inf). A softmax is scaled by the row's largest logit: 2^(r log2e - c), c
+// = max log2e rounded once, an error that all terms share and the factor takes
+// out. sigmoid(r) = e^min(r,0) / (1 + e^-|r|) needs one exponential where the
+// row has a logit >= 0; a row below zero is scaled by its largest logit too, so
+// that it keeps its ratios where the sigmoids underflow. A row of only -inf has
+// no probabilities: all zero. NaN gives NaN, as does +inf under the softmax.
 template <int G, int NV, bool SIG>
-__device__ __forceinline__ void row_probs(float* v, float* slope, int sub, int E) {
-  float m = -INFINITY;
-  bool nan = false;
+__device__ __forceinline__ float row_terms(float* v, float* slope) {
+  constexpr float L2E = 1.4426950408889634f;
+  float m = v[0];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (sub + G * i < E) {
-      m = fmaxf(m, v[i]);
-      nan |= v[i] != v[i];
-    }
+  for (int i = 1; i < NV; ++i) m = fmaxf(m, v[i]);
   m = group_max<G>(m);
-  if (SIG) m = fminf(m, 0.f);
   float s = 0.f;
+  if (SIG) {
+    const bool below = __any_sync(0xffffffffu, m < 0.f);  // warp-uniform
+    const float c = (m < 0.f && m != -INFINITY ? m : 0.f) * -L2E;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float z = 0.f;
-    if (sub + G * i < E && (m != -INFINITY || nan)) {
-      if (SIG) {
-        const float u = expf(-fabsf(v[i]));
-        const float r1 = __frcp_rn(1.f + u);
-        z = expf(fminf(v[i], 0.f) - m) * r1;
-        if (v[i] != v[i]) z = v[i];
-        slope[i] = v[i] >= 0.f ? u * r1 : r1;
-      } else {
-        z = expf(v[i] - m);
-      }
-    } else if (SIG) {
-      slope[i] = 0.f;
+    for (int i = 0; i < NV; ++i) {
+      const float u = ex2(fabsf(v[i]) * -L2E), r1 = rcp(1.f + u);
+      const bool pos = v[i] >= 0.f;
+      float top = pos ? 1.f : u;
+      if (below && !pos) top = ex2(fmaf(v[i], L2E, c));
+      slope[i] = (pos ? u : 1.f) * r1;
+      v[i] = top * r1;
+      s += v[i];
     }
-    v[i] = z;
-    s += z;
+  } else {
+    const float c = (m != -INFINITY ? m : 0.f) * -L2E;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      v[i] = ex2(fmaf(v[i], L2E, c));
+      s += v[i];
+    }
   }
   s = group_sum<G>(s);
-  const float inv = s == 0.f ? 0.f : 1.f / s;
+  return s == 0.f ? 0.f : rcp(s);
+}
+
+// One row's logits into registers (experts past E: -inf); rows that do not
+// exist or do not count: zeros, whatever they hold.
+template <typename TL, int G, int NV>
+__device__ __forceinline__ void load_row(const TL* row, bool ok, int sub, int E, float* v) {
+  const TL* p = row + sub;
+  if (E == G * NV) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] *= inv;
+    for (int i = 0; i < NV; ++i) v[i] = 0.f;
+    if (ok) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] = to_f32(p[G * i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      v[i] = sub + G * i < E ? (ok ? to_f32(p[G * i]) : 0.f) : -INFINITY;
+  }
 }
 
 // Deterministic block sum of a double (all threads get it); red holds 32.
@@ -168,29 +200,37 @@ __global__ void __launch_bounds__(THREADS) balance_kernel(const BalParams p) {
     for (int i = threadIdx.x; i < p.E; i += THREADS) s_cnt[i] = 0;
     if (threadIdx.x == 0) s_n = 0;
     __syncthreads();
-    float ps[NV];
+    float ps[NV], next[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) ps[i] = 0.f;
     int mine = 0;
+    // the next rows' logits are loaded before these are worked on
+    auto is_live = [&](int t) { return t < e && (p.mask == nullptr || p.mask[t] != 0); };
+    auto load = [&](int t, bool ok) {
+      load_row<TL, G, NV>(logits + (int64_t)t * p.ld, ok, sub, p.E, next);
+    };
+    bool next_live = is_live(b + warp * PER + grp);
+    load(b + warp * PER + grp, next_live);
     for (int t0 = b + warp * PER; t0 < e; t0 += WARPS * PER) {
       const int t = t0 + grp;
-      const bool live = t < e && (p.mask == nullptr || p.mask[t] != 0);
+      const bool live = next_live;
       float v[NV], slope[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int x = sub + G * i;
-        v[i] = (live && x < p.E) ? to_f32(logits[(int64_t)t * p.ld + x]) : 0.f;
-      }
-      if (live)
-        for (int j = sub; j < p.k; j += G) {
+      for (int i = 0; i < NV; ++i) v[i] = next[i];
+      int chosen = -1;
+      if (live && sub < p.k) chosen = p.idx[(int64_t)t * p.k + sub];
+      next_live = is_live(t + WARPS * PER);
+      load(t + WARPS * PER, next_live);
+      const float inv = row_terms<G, NV, SIG>(v, slope);
+      if (live) {
+        if ((unsigned)chosen < (unsigned)p.E) atomicAdd(&s_cnt[chosen], 1);
+        for (int j = sub + G; j < p.k; j += G) {
           const int x = p.idx[(int64_t)t * p.k + j];
           if ((unsigned)x < (unsigned)p.E) atomicAdd(&s_cnt[x], 1);
         }
-      row_probs<G, NV, SIG>(v, slope, sub, p.E);
-      if (live) {
         mine += sub == 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) ps[i] += v[i];
+        for (int i = 0; i < NV; ++i) ps[i] = fmaf(v[i], inv, ps[i]);
       }
     }
     // the groups of a warp hold the same experts: add them up
@@ -229,42 +269,42 @@ __global__ void __launch_bounds__(THREADS) balance_kernel(const BalParams p) {
   }
 }
 
-// One block per sequence: those that met several chunks add their slots up,
-// empty ones get zeros. 32 experts at a time, 32 slots of each in parallel.
+// One block of 1024 threads per sequence: those that met several chunks add
+// their slots up, empty ones get zeros. A thread per expert (rounded up to a
+// warp) and part of the slots; the parts are added in order.
 __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ double s_ps[32][33];
-  __shared__ int s_c[32][33];
+  __shared__ double s_ps[1024];
+  __shared__ int s_c[1024];
   __shared__ double s_red[32];
   const int s = blockIdx.x;
   const int qb = seq_begin(p.cu, s, p.T), qe = seq_end(p.cu, s, p.T);
   const bool empty = qb >= qe;
   const int f = empty ? 0 : qb / p.chunk, l = empty ? -1 : (qe - 1) / p.chunk;
   if (!empty && f == l) return;  // finished where it was read
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-  double dot = 0.0;
-  for (int e0 = 0; e0 < p.E; e0 += 32) {
-    const int e = e0 + lane;
-    double ps = 0.0;
-    int c = 0;
-    if (e < p.E)
-      for (int j = f + row; j <= l; j += 32) {
-        ps += (double)p.part_psum[((size_t)j + s) * p.E + e];
-        c += p.part_counts[((size_t)j + s) * p.E + e];
-      }
-    __syncthreads();
-    s_ps[row][lane] = ps;
-    s_c[row][lane] = c;
-    __syncthreads();
-    if (row == 0 && e < p.E) {
-      for (int w = 1; w < 32; ++w) {
-        ps += s_ps[w][lane];
-        c += s_c[w][lane];
-      }
-      p.counts[(size_t)s * p.E + e] = c;
-      dot += (double)c * ps;
+  const int width = (p.E + 31) & ~31, parts = 1024 / width;
+  const int e = threadIdx.x % width, part = threadIdx.x / width;
+  double ps = 0.0;
+  int c = 0;
+  if (e < p.E && part < parts) {
+#pragma unroll 4
+    for (int j = f + part; j <= l; j += parts) {
+      ps += (double)p.part_psum[((size_t)j + s) * p.E + e];
+      c += p.part_counts[((size_t)j + s) * p.E + e];
     }
+  }
+  s_ps[threadIdx.x] = ps;
+  s_c[threadIdx.x] = c;
+  __syncthreads();
+  double dot = 0.0;
+  if (part == 0 && e < p.E) {
+    for (int w = 1; w < parts; ++w) {
+      ps += s_ps[w * width + e];
+      c += s_c[w * width + e];
+    }
+    p.counts[(size_t)s * p.E + e] = c;
+    dot = (double)c * ps;
   }
   int n = 0;
   for (int j = f + (int)threadIdx.x; j <= l; j += blockDim.x) n += p.part_tokens[(size_t)j + s];
@@ -292,6 +332,13 @@ __global__ void __launch_bounds__(256) balance_backward_kernel(const BalParams p
   if (b64 >= p.T) return;  // warp-uniform
   const int b = (int)b64, e = min(p.T, b + run);
   const TL* logits = static_cast<const TL*>(p.logits);
+  // the next rows' logits are loaded before these are worked on, and the first
+  // before their sequence is looked up: rows that do not count are read as well
+  float next[NV];
+  auto load = [&](int t) {
+    load_row<TL, G, NV>(logits + (int64_t)t * p.ld, t < e, sub, p.E, next);
+  };
+  load(b + grp);
   int s = first_seq_past(p.cu, p.S, min(b + grp, p.T - 1)), have = -1;
   int qb = 0, qe = 0;
   float f[NV], coef = 0.f;
@@ -307,36 +354,41 @@ __global__ void __launch_bounds__(256) balance_backward_kernel(const BalParams p
     const bool live = inside && (p.mask == nullptr || p.mask[t] != 0);
     float v[NV], slope[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int x = sub + G * i;
-      v[i] = (live && x < p.E) ? to_f32(logits[(int64_t)t * p.ld + x]) : 0.f;
-    }
+    for (int i = 0; i < NV; ++i) v[i] = next[i];
+    load(t + PER);
     if (live && have != s) {
       have = s;
       const int n = p.tokens[s];
-      const double nk = (double)n * (double)p.k;
+      const int64_t nk = (int64_t)n * p.k;
       coef = n > 0 ? (float)((double)dloss[s] * (double)p.E / (double)n) : 0.f;
+      const float over = n > 0 ? (float)(1.0 / ((double)nk * (double)p.E)) : 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int x = sub + G * i;
-        f[i] = (x < p.E && n > 0)
-                   ? (float)(((double)p.counts[(size_t)s * p.E + x] * (double)p.E - nk) /
-                             (nk * (double)p.E))
-                   : 0.f;
+        f[i] = x < p.E ? (float)((int64_t)p.counts[(size_t)s * p.E + x] * p.E - nk) * over : 0.f;
       }
     }
-    row_probs<G, NV, SIG>(v, slope, sub, p.E);
+    const float inv = row_terms<G, NV, SIG>(v, slope);
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) dot = fmaf(f[i], v[i], dot);
-    dot = group_sum<G>(dot);
-    if (t < e) {
+    dot = group_sum<G>(dot) * inv;
+    const float k = coef * inv;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int x = sub + G * i;
-        float d = coef * v[i] * (f[i] - dot);
-        if (SIG) d *= slope[i];
-        if (x < p.E) dlogits[(int64_t)t * p.E + x] = from_f32<TL>(live ? d : 0.f);
+    for (int i = 0; i < NV; ++i) {
+      v[i] = v[i] * k * (f[i] - dot);
+      if (SIG) v[i] *= slope[i];
+      if (!live) v[i] = 0.f;
+    }
+    if (t < e) {
+      TL* o = dlogits + (int64_t)t * p.E + sub;
+      if (p.E == G * NV) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) o[G * i] = from_f32<TL>(v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (sub + G * i < p.E) o[G * i] = from_f32<TL>(v[i]);
       }
     }
   }

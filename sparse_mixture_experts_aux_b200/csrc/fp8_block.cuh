@@ -34,31 +34,57 @@ __device__ __forceinline__ float block_scale(float absmax) {
   return absmax == 0.f ? 1.f : (absmax != absmax ? absmax : fmaxf(absmax / 448.0f, FLT_MIN));
 }
 
-struct Divisor {
-  float scale, inv;
-  bool fast;
-  __device__ __forceinline__ explicit Divisor(float s) : scale(s) {
-    fast = s > 0x1p-80f && s < 0x1p100f;
-    inv = fast ? __frcp_rn(s) : 0.f;
-  }
-  __device__ __forceinline__ float of(float x) const {
-    const float q = x * inv;
-    return fmaf(fmaf(-q, scale, x), inv, q);
-  }
-};
-
 // Two fp32 -> two E4M3 codes (a in the low byte), round to nearest even, saturating.
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
-__device__ __forceinline__ uint32_t encode4(const float* f, const Divisor& d) {
-  if (d.fast)
-    return e4m3x2(d.of(f[0]), d.of(f[1])) | e4m3x2(d.of(f[2]), d.of(f[3])) << 16;
-  return e4m3x2(__fdiv_rn(f[0], d.scale), __fdiv_rn(f[1], d.scale)) |
-         e4m3x2(__fdiv_rn(f[2], d.scale), __fdiv_rn(f[3], d.scale)) << 16;
+__device__ __noinline__ uint32_t e4m3x4_by_division(float a, float b, float c, float d, float s) {
+  return e4m3x2(__fdiv_rn(a, s), __fdiv_rn(b, s)) |
+         e4m3x2(__fdiv_rn(c, s), __fdiv_rn(d, s)) << 16;
 }
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+struct Divisor {
+  float scale;
+  uint64_t inv2, neg2;  // 1 / scale and -scale, twice each
+  bool fast;
+  __device__ __forceinline__ explicit Divisor(float s) : scale(s) {
+    fast = s > 0x1p-80f && s < 0x1p100f;
+    const float inv = fast ? __frcp_rn(s) : 0.f;
+    inv2 = pack2(inv, inv);
+    neg2 = pack2(-s, -s);
+  }
+  // codes of a / scale and b / scale
+  __device__ __forceinline__ uint32_t codes2(float a, float b) const {
+    const uint64_t x = pack2(a, b);
+    uint64_t q;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(inv2));
+    q = fma2(fma2(q, neg2, x), inv2, q);
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(q));
+    return e4m3x2(lo, hi);
+  }
+};
+
+__device__ __forceinline__ uint32_t encode4(const float* f, const Divisor& d) {
+  if (d.fast) return d.codes2(f[0], f[1]) | d.codes2(f[2], f[3]) << 16;
+  return e4m3x4_by_division(f[0], f[1], f[2], f[3], d.scale);
+}
+
+// Row blocks a lane has in flight: 64 (bf16) or 128 (fp32) bytes of loads.
+template <typename TX> constexpr int ROW_UNITS = 2;
 
 // Sixteen consecutive elements held as raw 16-byte vectors.
 template <typename TX> struct Vec16E {
@@ -73,16 +99,25 @@ template <typename TX> struct Vec16E {
     for (int i = 0; i < NVEC; ++i) u[i] = make_uint4(0, 0, 0, 0);
   }
   __device__ __forceinline__ void values(int i, float* f) const { Vec16<TX>::unpack(u[i], f); }
+  // Largest magnitude. The bits of magnitudes order as integers do, NaNs above
+  // infinity: bf16 pairs are compared as two 16-bit integers at once.
   __device__ __forceinline__ float absmax() const {
-    float m = 0.f;
+    if (sizeof(TX) == 2) {
+      uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < NVEC; ++i) {
-      float f[Vec16<TX>::N];
-      values(i, f);
+      for (int i = 0; i < NVEC; ++i) {
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
-      for (int j = 0; j < Vec16<TX>::N; ++j) m = max_nan(m, fabsf(f[j]));
+        for (int j = 0; j < 4; ++j) m = __vmaxu2(m, w[j] & 0x7fff7fffu);
+      }
+      return __uint_as_float(max(m << 16, m & 0xffff0000u));
     }
-    return m;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < NVEC; ++i)
+      m = max(max(max(m, u[i].x & 0x7fffffffu), max(u[i].y & 0x7fffffffu, u[i].z & 0x7fffffffu)),
+              u[i].w & 0x7fffffffu);
+    return __uint_as_float(m);
   }
   __device__ __forceinline__ uint4 codes(const Divisor& d) const {
     uint32_t w[4];
@@ -98,46 +133,59 @@ template <typename TX> struct Vec16E {
   }
 };
 
-// 1 x 128 blocks: eight lanes a block, sixteen elements a lane.
+// 1 x 128 blocks: eight lanes a block, sixteen elements a lane, UNITS blocks a
+// lane whose loads are all in flight before the first is used.
 template <typename TX>
 __global__ void __launch_bounds__(256) quantize_row_blocks_kernel(
-    const TX* __restrict__ x, int64_t rows, int cols, int64_t ld, uint8_t* __restrict__ codes,
-    float* __restrict__ scales) {
+    const TX* __restrict__ x, int64_t rows, int cols, int64_t ld, int step_r, int step_b,
+    uint8_t* __restrict__ codes, float* __restrict__ scales) {
   pdl_wait();
   pdl_launch_dependents();
+  constexpr int UNITS = ROW_UNITS<TX>;
   const int kb = (cols + BLK - 1) / BLK;
   const int64_t units = rows * kb;  // blocks
   const int sub = threadIdx.x & 7;
-  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> 3);
-  // whole warps take part in the shuffles: the bound is rounded up to a warp's four blocks
-  for (int64_t u0 = (int64_t)blockIdx.x * (blockDim.x >> 3) + (threadIdx.x >> 5) * 4; u0 < units;
-       u0 += step) {
-    const int64_t u = u0 + ((threadIdx.x & 31) >> 3);
-    int64_t r;
-    int b;
-    if (units <= 0x7fffffff) {
-      r = (uint32_t)u / (uint32_t)kb;
-      b = (int)((uint32_t)u - (uint32_t)r * (uint32_t)kb);
-    } else {
-      r = u / kb;
-      b = (int)(u - r * kb);
-    }
+  const int64_t u0 = (int64_t)blockIdx.x * (32 * UNITS) + (threadIdx.x >> 3);
+  Vec16E<TX> v[UNITS];
+  int64_t at[UNITS];  // where this lane's codes go, -1 behind the last column or block
+  int64_t r;
+  int b;
+  if (units <= 0x7fffffff) {
+    r = (uint32_t)u0 / (uint32_t)kb;
+    b = (int)((uint32_t)u0 - (uint32_t)r * (uint32_t)kb);
+  } else {
+    r = u0 / kb;
+    b = (int)(u0 - r * kb);
+  }
+#pragma unroll
+  for (int i = 0; i < UNITS; ++i) {
     const int c = b * BLK + sub * 16;
-    const bool in = u < units && c < cols;
-    Vec16E<TX> v;
-    if (in) v.load(x + r * ld + c); else v.zero();
-    float m = v.absmax();
+    at[i] = r < rows && c < cols ? r * cols + c : -1;
+    if (at[i] >= 0) v[i].load(x + r * ld + c); else v[i].zero();
+    r += step_r;  // 32 blocks on: 32 = step_r kb + step_b
+    b += step_b;
+    if (b >= kb) {
+      b -= kb;
+      ++r;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < UNITS; ++i) {
+    float m = v[i].absmax();
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float s = block_scale(m);
-    if (in) st_v4(codes + r * cols + c, v.codes(Divisor(s)));
-    if (u < units && sub == 0) scales[u] = s;
+    if (at[i] >= 0) {
+      st_v4(codes + at[i], v[i].codes(Divisor(s)));
+      if (sub == 0) scales[u0 + 32 * i] = s;
+    }
   }
 }
 
-// 128 x 128 blocks: one block of 256 threads each, 64 elements a thread.
+// 128 x 128 blocks: one block of 256 threads each, 64 elements a thread; four
+// (fp32: two) blocks an SM, so that one's loads cover another's arithmetic.
 template <typename TX>
-__global__ void __launch_bounds__(256) quantize_square_blocks_kernel(
+__global__ void __launch_bounds__(256, sizeof(TX) == 2 ? 4 : 2) quantize_square_blocks_kernel(
     const TX* __restrict__ x, int64_t rows, int cols, int64_t ld, int nb, int kb,
     uint8_t* __restrict__ codes, float* __restrict__ scales) {
   pdl_wait();

@@ -1021,7 +1021,7 @@ moe_status check_balance(const moe_balance_dims* d) {
 // least 32 tokens. Depends on T alone, so the workspace size does too.
 int balance_chunk(int64_t T) {
   const int64_t c = (T + 147) / 148;
-  return static_cast<int>(c < 32 ? 32 : c);
+  return static_cast<int>(c < MOE_BALANCE_SMALL_T ? MOE_BALANCE_SMALL_T : c);
 }
 size_t balance_slots(const moe_balance_dims* d) {
   const int64_t ch = balance_chunk(d->T);
@@ -1420,10 +1420,10 @@ moe_status moe_balance_loss(const moe_balance_dims* dims, const void* logits,
       (dims->T > 0 && (logits == nullptr || topk_idx == nullptr || !aligned(logits, el) ||
                        !aligned(topk_idx, 4))))
     return MOE_ERR_INVALID_ARG;
-  if (dims->workspace == nullptr || !aligned(dims->workspace, 256) ||
-      dims->workspace_bytes < moe_balance_loss_workspace_size(dims))
-    return MOE_ERR_WORKSPACE;
   moe::bal::BalParams p = balance_params(dims, logits);
+  if (p.nchunks > 1 && (dims->workspace == nullptr || !aligned(dims->workspace, 256) ||
+                        dims->workspace_bytes < moe_balance_loss_workspace_size(dims)))
+    return MOE_ERR_WORKSPACE;
   const size_t cells = balance_slots(dims) * static_cast<size_t>(p.E);
   p.idx = topk_idx;
   p.part_psum = static_cast<float*>(dims->workspace);
@@ -1487,14 +1487,18 @@ moe_status moe_quantize_fp8_block(const void* w, int32_t dtype, int64_t stack, i
   const int64_t kb = (cols + moe::f8b::BLK - 1) / moe::f8b::BLK;
   if (block_rows == 1) {
     const int64_t n = stack * rows;
-    const int64_t blocks = (n * kb + 31) / 32;
-    const unsigned grid = static_cast<unsigned>(blocks < 148 * 64 ? blocks : 148 * 64);
+    const int64_t per = 32 * (dtype == MOE_BF16 ? moe::f8b::ROW_UNITS<__nv_bfloat16>
+                                                : moe::f8b::ROW_UNITS<float>);
+    if ((n * kb + per - 1) / per >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    const unsigned grid = static_cast<unsigned>((n * kb + per - 1) / per);
     if (dtype == MOE_BF16)
       launch_pdl(moe::f8b::quantize_row_blocks_kernel<__nv_bfloat16>, grid, 256, 0, st,
-                 static_cast<const __nv_bfloat16*>(w), n, cols, ld, codes, scales);
+                 static_cast<const __nv_bfloat16*>(w), n, cols, ld, static_cast<int>(32 / kb),
+                 static_cast<int>(32 % kb), codes, scales);
     else
       launch_pdl(moe::f8b::quantize_row_blocks_kernel<float>, grid, 256, 0, st,
-                 static_cast<const float*>(w), n, cols, ld, codes, scales);
+                 static_cast<const float*>(w), n, cols, ld, static_cast<int>(32 / kb),
+                 static_cast<int>(32 % kb), codes, scales);
     return launched();
   }
   const int64_t nb = (rows + moe::f8b::BLK - 1) / moe::f8b::BLK;

@@ -7,7 +7,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from .balance import _handle, _lend, _need
+from .balance import _handle, _lend, _need, _on
 from .layer import dtype_code
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)
@@ -38,10 +38,10 @@ def quantize_fp8_block(w: torch.Tensor, block_rows: int = 128, stream=None):
     for n in w.shape[:-2]:
         stack *= n
     dev = w.device
-    with torch.cuda.device(dev):
+    with _on(dev):
         codes = torch.empty(w.shape, dtype=torch.uint8, device=dev)
-        srows = (rows,) if block_rows == 1 else (_ceil(rows, max(1, block_rows)),)
-        scales = torch.empty(w.shape[:-2] + srows + (_ceil(cols, 128),), dtype=torch.float32,
+        srows = rows if block_rows == 1 else _ceil(rows, max(1, block_rows))
+        scales = torch.empty((*w.shape[:-2], srows, _ceil(cols, 128)), dtype=torch.float32,
                              device=dev)
         for t in (codes, scales):
             _lend(t, stream)
@@ -63,7 +63,7 @@ def dequantize_fp8_block(codes: torch.Tensor, scales: torch.Tensor, block_rows: 
     dev = codes.device
     srows = rows if block_rows == 1 else _ceil(rows, max(1, block_rows))
     _need("scales", scales, torch.float32, codes.shape[:-2] + (srows, _ceil(cols, 128)), dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         out = torch.empty(codes.shape, dtype=torch.float32, device=dev)
         _lend(out, stream)
         if codes.numel() == 0 and cols > 0:
@@ -100,12 +100,9 @@ def _product_dims(a, a_scales, weights, scales, offsets, wait_timeout_ns):
         _need("weights", t, _CODES, lead + (N, K), dev)
         _need("weight scales", s, torch.float32, lead + (_ceil(N, 128), _ceil(K, 128)), dev)
     _need("a_scales", a_scales, torch.float32, (M, _ceil(K, 128)), dev)
-    d = _lib.moe_fp8_block_dims()
-    d.M, d.N, d.K, d.E = M, N, K, E
-    d.lda = a.stride(0) if M > 1 else K
-    d.offsets = offsets.data_ptr() if E else None
-    d.wait_timeout_ns = int(wait_timeout_ns)
-    return d, M, N
+    fields = (M, N, K, E, 0, a.stride(0) if M > 1 else K, 0,
+              offsets.data_ptr() if E else None, None, int(wait_timeout_ns))
+    return _lib.moe_fp8_block_dims(*fields), M, N
 
 
 def matmul_fp8_block(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor,
@@ -129,7 +126,7 @@ def matmul_fp8_block(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor,
     if row_scale is not None:
         _need("row_scale", row_scale, torch.float32, (M,), dev)
         d.row_scale = row_scale.data_ptr()
-    with torch.cuda.device(dev):
+    with _on(dev):
         if out is None:
             out = torch.empty(M, N, dtype=out_dtype, device=dev)
             _lend(out, stream)
@@ -160,7 +157,7 @@ def swiglu_fp8_block(a: torch.Tensor, a_scales: torch.Tensor, W_g: torch.Tensor,
     """
     d, M, N = _product_dims(a, a_scales, (W_g, W_u), (g_scales, u_scales), offsets, wait_timeout_ns)
     dev = a.device
-    with torch.cuda.device(dev):
+    with _on(dev):
         if codes is None:
             codes = torch.empty(M, N, dtype=torch.uint8, device=dev)
             _lend(codes, stream)
