@@ -63,17 +63,6 @@ __device__ __forceinline__ int first_seq_past(const int32_t* cu, int S, int t) {
   return lo;
 }
 
-template <int G> __device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-template <int G> __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
 // 2^x and 1/x by the hardware: off by 2 ulp and 1 ulp, results below 2^-126 are
 // zero. With the library's expf and a true division, and a test of every
 // expert's index, a row of 256 took 540 instructions forward and 740 backward
@@ -98,38 +87,55 @@ __device__ __forceinline__ float rcp(float x) {
 // row has a logit >= 0; a row below zero is scaled by its largest logit too, so
 // that it keeps its ratios where the sigmoids underflow. A row of only -inf has
 // no probabilities: all zero. NaN gives NaN, as does +inf under the softmax.
-template <int G, int NV, bool SIG>
-__device__ __forceinline__ float row_terms(float* v, float* slope) {
+// U rows at once, so that their shuffles overlap.
+template <int G, int NV, int U, bool SIG>
+__device__ __forceinline__ void row_terms(float (*v)[NV], float (*slope)[NV], float* inv) {
   constexpr float L2E = 1.4426950408889634f;
-  float m = v[0];
+  float m[U], s[U];
 #pragma unroll
-  for (int i = 1; i < NV; ++i) m = fmaxf(m, v[i]);
-  m = group_max<G>(m);
-  float s = 0.f;
-  if (SIG) {
-    const bool below = __any_sync(0xffffffffu, m < 0.f);  // warp-uniform
-    const float c = (m < 0.f && m != -INFINITY ? m : 0.f) * -L2E;
+  for (int u = 0; u < U; ++u) {
+    m[u] = v[u][0];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const float u = ex2(fabsf(v[i]) * -L2E), r1 = rcp(1.f + u);
-      const bool pos = v[i] >= 0.f;
-      float top = pos ? 1.f : u;
-      if (below && !pos) top = ex2(fmaf(v[i], L2E, c));
-      slope[i] = (pos ? u : 1.f) * r1;
-      v[i] = top * r1;
-      s += v[i];
-    }
-  } else {
-    const float c = (m != -INFINITY ? m : 0.f) * -L2E;
+    for (int i = 1; i < NV; ++i) m[u] = fmaxf(m[u], v[u][i]);
+  }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      v[i] = ex2(fmaf(v[i], L2E, c));
-      s += v[i];
+  for (int o = G / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int u = 0; u < U; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    s[u] = 0.f;
+    if (SIG) {
+      const bool below = __any_sync(0xffffffffu, m[u] < 0.f);  // warp-uniform
+      const float c = (m[u] < 0.f && m[u] != -INFINITY ? m[u] : 0.f) * -L2E;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const float e = ex2(fabsf(v[u][i]) * -L2E), r1 = rcp(1.f + e);
+        const bool pos = v[u][i] >= 0.f;
+        float top = pos ? 1.f : e;
+        if (below && !pos) top = ex2(fmaf(v[u][i], L2E, c));
+        slope[u][i] = (pos ? e : 1.f) * r1;
+        v[u][i] = top * r1;
+        s[u] += v[u][i];
+      }
+    } else {
+      const float c = (m[u] != -INFINITY ? m[u] : 0.f) * -L2E;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        v[u][i] = ex2(fmaf(v[u][i], L2E, c));
+        s[u] += v[u][i];
+      }
     }
   }
-  s = group_sum<G>(s);
-  return s == 0.f ? 0.f : rcp(s);
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int u = 0; u < U; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+#pragma unroll
+  for (int u = 0; u < U; ++u) inv[u] = s[u] == 0.f ? 0.f : rcp(s[u]);
 }
+// Rows a group of lanes works on at once.
+template <int NV> constexpr int ROWS_AT_ONCE = NV <= 2 ? 4 : (NV == 4 ? 2 : 1);
 
 // One row's logits into registers (experts past E: -inf); rows that do not
 // exist or do not count: zeros, whatever they hold.
@@ -170,7 +176,7 @@ __device__ __forceinline__ float loss_of(double dot, int n, int E, int k) {
 }
 
 // One block per chunk of tokens; warps take the chunk's tokens in turn, 32 / G
-// at a time. The block walks the sequences that its chunk meets; each leaves
+// times ROWS_AT_ONCE at a time. The block walks the sequences that its chunk meets; each leaves
 // its sums in slot (chunk + sequence), which no other pair has, or, when the
 // sequence lies inside the chunk, its results at once.
 // Dynamic shared memory: float psum[warps][E], int32 counts[E].
@@ -179,7 +185,7 @@ __global__ void __launch_bounds__(THREADS) balance_kernel(const BalParams p) {
   pdl_wait();
   pdl_launch_dependents();
   extern __shared__ __align__(16) uint8_t bal_smem[];
-  constexpr int WARPS = THREADS / 32, PER = 32 / G;
+  constexpr int WARPS = THREADS / 32, U = ROWS_AT_ONCE<NV>, PER = 32 / G * U;
   float* s_psum = reinterpret_cast<float*>(bal_smem);
   int32_t* s_cnt = reinterpret_cast<int32_t*>(s_psum + (size_t)WARPS * p.E);
   __shared__ double s_red[32];
@@ -189,48 +195,68 @@ __global__ void __launch_bounds__(THREADS) balance_kernel(const BalParams p) {
   const TL* logits = static_cast<const TL*>(p.logits);
   const int c0 = blockIdx.x * p.chunk;
   const int c1 = min(p.T, c0 + p.chunk);
-  const bool alone = p.nchunks == 1;  // empty sequences are this block's too
-
-  for (int s = alone ? 0 : first_seq_past(p.cu, p.S, c0); s < p.S; ++s) {
+  if (p.nchunks == 1 && (p.cu != nullptr || p.T == 0)) {  // empty sequences: no other kernel sees them
+    for (int i = threadIdx.x; i < p.S * p.E; i += THREADS) {
+      const int s = i / p.E;
+      if (seq_begin(p.cu, s, p.T) >= seq_end(p.cu, s, p.T)) {
+        p.counts[i] = 0;
+        if (i == s * p.E) {
+          p.tokens[s] = 0;
+          p.loss[s] = 0.f;
+        }
+      }
+    }
+  }
+  for (int s = first_seq_past(p.cu, p.S, c0); s < p.S; ++s) {
     const int qb = seq_begin(p.cu, s, p.T), qe = seq_end(p.cu, s, p.T);
-    if (!alone && qb >= c1) break;
+    if (qb >= c1) break;
     const int b = max(qb, c0), e = min(qe, c1);
-    if (!alone && b >= e) continue;
+    if (b >= e) continue;
     __syncthreads();
     for (int i = threadIdx.x; i < p.E; i += THREADS) s_cnt[i] = 0;
     if (threadIdx.x == 0) s_n = 0;
     __syncthreads();
-    float ps[NV], next[NV];
+    float ps[NV], next[U][NV];
+    bool next_live[U];
 #pragma unroll
     for (int i = 0; i < NV; ++i) ps[i] = 0.f;
     int mine = 0;
     // the next rows' logits are loaded before these are worked on
-    auto is_live = [&](int t) { return t < e && (p.mask == nullptr || p.mask[t] != 0); };
-    auto load = [&](int t, bool ok) {
-      load_row<TL, G, NV>(logits + (int64_t)t * p.ld, ok, sub, p.E, next);
-    };
-    bool next_live = is_live(b + warp * PER + grp);
-    load(b + warp * PER + grp, next_live);
-    for (int t0 = b + warp * PER; t0 < e; t0 += WARPS * PER) {
-      const int t = t0 + grp;
-      const bool live = next_live;
-      float v[NV], slope[NV];
+    auto load = [&](int t0) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = next[i];
-      int chosen = -1;
-      if (live && sub < p.k) chosen = p.idx[(int64_t)t * p.k + sub];
-      next_live = is_live(t + WARPS * PER);
-      load(t + WARPS * PER, next_live);
-      const float inv = row_terms<G, NV, SIG>(v, slope);
-      if (live) {
-        if ((unsigned)chosen < (unsigned)p.E) atomicAdd(&s_cnt[chosen], 1);
+      for (int u = 0; u < U; ++u) {
+        const int t = t0 + u * (32 / G) + grp;
+        next_live[u] = t < e && (p.mask == nullptr || p.mask[t] != 0);
+        load_row<TL, G, NV>(logits + (int64_t)t * p.ld, next_live[u], sub, p.E, next[u]);
+      }
+    };
+    load(b + warp * PER);
+    for (int t0 = b + warp * PER; t0 < e; t0 += WARPS * PER) {
+      float v[U][NV], slope[U][NV], inv[U];
+      bool live[U];
+      int chosen[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        live[u] = next_live[u];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[u][i] = next[u][i];
+        const int t = t0 + u * (32 / G) + grp;
+        chosen[u] = live[u] && sub < p.k ? p.idx[(int64_t)t * p.k + sub] : -1;
+      }
+      load(t0 + WARPS * PER);
+      row_terms<G, NV, U, SIG>(v, slope, inv);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!live[u]) continue;
+        const int t = t0 + u * (32 / G) + grp;
+        if ((unsigned)chosen[u] < (unsigned)p.E) atomicAdd(&s_cnt[chosen[u]], 1);
         for (int j = sub + G; j < p.k; j += G) {
           const int x = p.idx[(int64_t)t * p.k + j];
           if ((unsigned)x < (unsigned)p.E) atomicAdd(&s_cnt[x], 1);
         }
         mine += sub == 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) ps[i] = fmaf(v[i], inv, ps[i]);
+        for (int i = 0; i < NV; ++i) ps[i] = fmaf(v[u][i], inv[u], ps[i]);
       }
     }
     // the groups of a warp hold the same experts: add them up
@@ -316,7 +342,7 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalParams p)
   }
 }
 
-// The gradient: each warp takes `run` consecutive tokens, 32 / G at a time.
+// The gradient: each warp takes `run` consecutive tokens, as many at a time.
 // f - 1/E stands for f: the p of a row add up to 1, so the difference is the
 // same, and (c E - n k) is an exact integer, so an f near 1/E does not cancel.
 // Rows that are masked or lie in no sequence get zeros, whatever they hold.
@@ -325,7 +351,7 @@ __global__ void __launch_bounds__(256) balance_backward_kernel(const BalParams p
                                                                TL* dlogits, int run) {
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int PER = 32 / G;
+  constexpr int U = ROWS_AT_ONCE<NV>, PER = 32 / G * U;
   const int lane = threadIdx.x & 31, sub = lane & (G - 1), grp = lane / G;
   const int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int64_t b64 = w * run;
@@ -334,11 +360,15 @@ __global__ void __launch_bounds__(256) balance_backward_kernel(const BalParams p
   const TL* logits = static_cast<const TL*>(p.logits);
   // the next rows' logits are loaded before these are worked on, and the first
   // before their sequence is looked up: rows that do not count are read as well
-  float next[NV];
-  auto load = [&](int t) {
-    load_row<TL, G, NV>(logits + (int64_t)t * p.ld, t < e, sub, p.E, next);
+  float next[U][NV];
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u * (32 / G) + grp;
+      load_row<TL, G, NV>(logits + (int64_t)t * p.ld, t < e, sub, p.E, next[u]);
+    }
   };
-  load(b + grp);
+  load(b);
   int s = first_seq_past(p.cu, p.S, min(b + grp, p.T - 1)), have = -1;
   int qb = 0, qe = 0;
   float f[NV], coef = 0.f;
@@ -346,49 +376,56 @@ __global__ void __launch_bounds__(256) balance_backward_kernel(const BalParams p
   for (int i = 0; i < NV; ++i) f[i] = 0.f;
   if (s < p.S) { qb = seq_begin(p.cu, s, p.T); qe = seq_end(p.cu, s, p.T); }
   for (int t0 = b; t0 < e; t0 += PER) {
-    const int t = t0 + grp;
-    while (s < p.S && t >= qe) {
-      if (++s < p.S) { qb = seq_begin(p.cu, s, p.T); qe = seq_end(p.cu, s, p.T); }
-    }
-    const bool inside = t < e && s < p.S && t >= qb;
-    const bool live = inside && (p.mask == nullptr || p.mask[t] != 0);
-    float v[NV], slope[NV];
+    float v[U][NV], slope[U][NV], inv[U];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = next[i];
-    load(t + PER);
-    if (live && have != s) {
-      have = s;
-      const int n = p.tokens[s];
-      const int64_t nk = (int64_t)n * p.k;
-      coef = n > 0 ? (float)((double)dloss[s] * (double)p.E / (double)n) : 0.f;
-      const float over = n > 0 ? (float)(1.0 / ((double)nk * (double)p.E)) : 0.f;
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[u][i] = next[u][i];
+    load(t0 + PER);
+    row_terms<G, NV, U, SIG>(v, slope, inv);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u * (32 / G) + grp;
+      while (s < p.S && t >= qe) {
+        if (++s < p.S) { qb = seq_begin(p.cu, s, p.T); qe = seq_end(p.cu, s, p.T); }
+      }
+      const bool live =
+          t < e && s < p.S && t >= qb && (p.mask == nullptr || p.mask[t] != 0);
+      if (live && have != s) {
+        have = s;
+        const int n = p.tokens[s];
+        const int64_t nk = (int64_t)n * p.k;
+        coef = n > 0 ? (float)((double)dloss[s] * (double)p.E / (double)n) : 0.f;
+        const float over = n > 0 ? (float)(1.0 / ((double)nk * (double)p.E)) : 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int x = sub + G * i;
+          f[i] = x < p.E ? (float)((int64_t)p.counts[(size_t)s * p.E + x] * p.E - nk) * over : 0.f;
+        }
+      }
+      float dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) dot = fmaf(f[i], v[u][i], dot);
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      dot *= inv[u];
+      const float k = coef * inv[u];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int x = sub + G * i;
-        f[i] = x < p.E ? (float)((int64_t)p.counts[(size_t)s * p.E + x] * p.E - nk) * over : 0.f;
+        float d = v[u][i] * k * (f[i] - dot);
+        if (SIG) d *= slope[u][i];
+        v[u][i] = live ? d : 0.f;
       }
-    }
-    const float inv = row_terms<G, NV, SIG>(v, slope);
-    float dot = 0.f;
+      if (t < e) {
+        TL* o = dlogits + (int64_t)t * p.E + sub;
+        if (p.E == G * NV) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) dot = fmaf(f[i], v[i], dot);
-    dot = group_sum<G>(dot) * inv;
-    const float k = coef * inv;
+          for (int i = 0; i < NV; ++i) o[G * i] = from_f32<TL>(v[u][i]);
+        } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      v[i] = v[i] * k * (f[i] - dot);
-      if (SIG) v[i] *= slope[i];
-      if (!live) v[i] = 0.f;
-    }
-    if (t < e) {
-      TL* o = dlogits + (int64_t)t * p.E + sub;
-      if (p.E == G * NV) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) o[G * i] = from_f32<TL>(v[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (sub + G * i < p.E) o[G * i] = from_f32<TL>(v[i]);
+          for (int i = 0; i < NV; ++i)
+            if (sub + G * i < p.E) o[G * i] = from_f32<TL>(v[u][i]);
+        }
       }
     }
   }

@@ -37,7 +37,7 @@
 // row's sums depend on that row alone). A tile of few rows loads a smaller box
 // of A, and warps whose 32 rows are all behind the end skip their arithmetic.
 //
-// SPLIT (dense, few tiles): a cluster of S CTAs shares one tile, each sums a
+// SPLIT (few tiles): a cluster of S CTAs shares one tile, each sums a
 // range of K blocks, and the partial sums are added in rank order through
 // distributed shared memory (in the then idle operand ring): no workspace, no
 // atomics, the same bits every time.
@@ -196,32 +196,45 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(p));
   return p != 0u;
 }
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+  a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+}
+__device__ __forceinline__ uint2 bf16x4(const float* v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
 struct Tile {
   int e, nb, row0, valid;
 };
 
-// First row and rows of expert e, clamped so that any contents of the arrays
-// stay inside [0, M).
-__device__ __forceinline__ void segment(const Params& p, int e, int* start, int* len) {
-  int64_t b = 0, t = p.M;
-  if (p.offsets != nullptr) {
-    b = p.offsets[e];
-    t = p.offsets[e + 1];
-  } else if (p.tile_start != nullptr) {
-    b = (int64_t)p.tile_start[e] * ROW_TILE;
-    const int64_t c = p.counts[e];
-    t = b + (p.cap >= 0 && c > p.cap ? p.cap : c);
+// What the arrays say of expert e, and from that its first row and rows, clamped
+// so that any contents of the arrays stay inside [0, M).
+__device__ __forceinline__ int2 segment_load(const Params& p, int e) {
+  if (p.offsets != nullptr) return make_int2(p.offsets[e], p.offsets[e + 1]);
+  if (p.tile_start != nullptr) return make_int2(p.tile_start[e], p.counts[e]);
+  return make_int2(0, p.M);
+}
+__device__ __forceinline__ int2 segment_of(const Params& p, int2 raw) {
+  int64_t b = raw.x, t = raw.y;
+  if (p.offsets == nullptr && p.tile_start != nullptr) {
+    b *= ROW_TILE;
+    t = b + (p.cap >= 0 && t > p.cap ? p.cap : t);
   }
   b = b < 0 ? 0 : (b > p.M ? p.M : b);
   t = t < b ? b : (t > p.M ? p.M : t);
-  *start = (int)b;
-  *len = (int)(t - b);
+  return make_int2((int)b, (int)(t - b));
 }
 
 // Tile order: expert by expert; within an expert the row tiles are fastest, so
 // CTAs running at the same time share weight tiles through L2. s_mt: first row
 // tile of each expert.
-__device__ __forceinline__ Tile decode(int tile, const Params& p, const int32_t* s_mt) {
+// In two steps, locate and place, so that the loads in between can be in flight.
+struct Place {
+  int e, nb, mi;
+  int2 raw;
+};
+__device__ __forceinline__ Place locate(int tile, const Params& p, const int32_t* s_mt) {
   const int q = tile / p.n_tiles;
   int lo = 0, hi = p.E - 1;  // last expert whose first row tile is at or before q
   while (lo < hi) {
@@ -230,14 +243,20 @@ __device__ __forceinline__ Tile decode(int tile, const Params& p, const int32_t*
   }
   const int me = s_mt[lo + 1] - s_mt[lo];
   const int in_e = tile - p.n_tiles * s_mt[lo];
-  const int nb = in_e / me, mi = in_e - nb * me;
-  int start, len;
-  segment(p, lo, &start, &len);
+  Place l;
+  l.e = lo;
+  l.nb = in_e / me;
+  l.mi = in_e - l.nb * me;
+  l.raw = segment_load(p, lo);
+  return l;
+}
+__device__ __forceinline__ Tile place(const Place& l, const Params& p) {
+  const int2 seg = segment_of(p, l.raw);
   Tile t;
-  t.e = lo;
-  t.nb = nb;
-  t.row0 = start + mi * BM;
-  t.valid = min(BM, len - mi * BM);
+  t.e = l.e;
+  t.nb = l.nb;
+  t.row0 = seg.x + l.mi * BM;
+  t.valid = min(BM, seg.y - l.mi * BM);
   return t;
 }
 
@@ -378,8 +397,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int run = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
-      int start, len = 0;
-      if (e < p.E) segment(p, e, &start, &len);
+      const int len = e < p.E ? segment_of(p, segment_load(p, e)).y : 0;
       const int v = (len + BM - 1) / BM;
       int incl = v;
 #pragma unroll
@@ -413,8 +431,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t issued = 0, last_par = 0, phase = 0;
       int stage = 0;
       bool ok = true;
+      Place next{};
+      if (first < total) next = locate(first, p, s_mt);
       for (int tile = first; ok && tile < total; tile += step) {
-        const Tile t = decode(tile, p, s_mt);
+        const Tile t = place(next, p);
         const int box = t.valid <= 16 ? 0 : (t.valid <= 64 ? 1 : 2);
         const uint32_t bytes = (box == 0 ? 16 : (box == 1 ? 64 : 128)) * BLK + B_BYTES;
         const int n0 = MODE == SWIGLU ? t.nb * BLK : t.nb * BN;
@@ -433,6 +453,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             MODE == SWIGLU ? n0 : n0 + BLK, t.e);
           }
           __syncwarp();
+          // the next tile is looked up behind this one's first copy, so that no copy
+          // waits for the look-up's loads
+          if (kb == kb0 && tile + step < total) next = locate(tile + step, p, s_mt);
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -481,7 +504,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int tile = first; ok && tile < total; tile += step) {
-        const Tile t = decode(tile, p, s_mt);
+        const Tile t = place(locate(tile, p, s_mt), p);
         const int b0 = MODE == SWIGLU ? t.nb : 2 * t.nb;
         const int b1 = MODE == SWIGLU ? t.nb : min(2 * t.nb + 1, p.n_blocks - 1);
         const float* w0 = p.w_scale0 + ((int64_t)t.e * p.n_blocks + b0) * p.k_blocks;
@@ -651,54 +674,83 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncthreads();
     tc2::cluster_sync();  // every rank's partial sums are in its ring
     if (warp >= FIRST_EPI_WARP && first < total && !*abort_flag) {
-      const Tile t = decode(first, p, s_mt);
+      const Tile t = place(locate(first, p, s_mt), p);
       const int w = warp - FIRST_EPI_WARP;
-      if (MODE == MATMUL) {
-        // a warp adds up 128 columns of one row, four a lane
-        for (int u = rank + ranks * w; u < 2 * t.valid; u += ranks * EPI_WARPS) {
-          const int r = u >> 1, col = (u & 1) * 128 + lane * 4;
-          const uint32_t at = stage0 + (r * DUMP_LD + col) * 4;
-          float v[4] = {0.f, 0.f, 0.f, 0.f};
-          for (uint32_t k = 0; k < ranks; ++k) {
-            const float4 x = ld_cluster_v4(tc2::mapa_shared(at, k));
-            v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-          }
-          const int64_t row = (int64_t)t.row0 + r;
-          const float f = p.row_scale != nullptr ? p.row_scale[row] : 1.f;
+      // A warp takes four rows at a time, a lane four columns of each half of the
+      // tile; the sums of two ranks are in flight at once and added in rank order.
+      constexpr int R = 4;
+      const int stride = (int)ranks * EPI_WARPS;
+      for (int r0 = (int)rank + (int)ranks * w; r0 < t.valid; r0 += stride * R) {
+        float4 lo[R], hi[R];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int n = t.nb * BN + col + i;
-            if (n < p.N) {
-              if (p.out_f32) static_cast<float*>(p.out)[row * p.out_ld + n] = f * v[i];
-              else static_cast<__nv_bfloat16*>(p.out)[row * p.out_ld + n] = __float2bfloat16_rn(f * v[i]);
+        for (int i = 0; i < R; ++i) lo[i] = hi[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (uint32_t k = 0; k < ranks; k += 2) {
+          float4 x[2][R], y[2][R];
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+              const int r = r0 + i * stride;
+              x[kk][i] = y[kk][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (k + kk < ranks && r < t.valid) {
+                const uint32_t a =
+                    tc2::mapa_shared(stage0 + (r * DUMP_LD + lane * 4) * 4, k + kk);
+                x[kk][i] = ld_cluster_v4(a);
+                y[kk][i] = ld_cluster_v4(a + 512);
+              }
             }
-          }
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+              add4(lo[i], x[kk][i]);
+              add4(hi[i], y[kk][i]);
+            }
         }
-      } else {
-        for (int r = rank + ranks * w; r < t.valid; r += ranks * EPI_WARPS) {
-          const uint32_t at = stage0 + (r * DUMP_LD + lane * 4) * 4;
-          float g[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-          for (uint32_t k = 0; k < ranks; ++k) {
-            const uint32_t a = tc2::mapa_shared(at, k);
-            const float4 x = ld_cluster_v4(a), y = ld_cluster_v4(a + 512);
-            g[0] += x.x; g[1] += x.y; g[2] += x.z; g[3] += x.w;
-            u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
-          }
-          const int col = t.nb * BLK + lane * 4;
-          float m = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            g[i] = silu_f32(g[i]) * u[i];
-            if (col < p.N) m = max_nan(m, fabsf(g[i]));
-          }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const float s = block_scale(m);
+        for (int i = 0; i < R; ++i) {
+          const int r = r0 + i * stride;
+          if (r >= t.valid) break;  // warp-uniform
           const int64_t row = (int64_t)t.row0 + r;
-          if (col < p.N)
-            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + row * p.out_ld + col) =
-                encode4(g, Divisor(s));
-          if (lane == 0) p.out_scale[row * p.n_blocks + t.nb] = s;
+          if (MODE == MATMUL) {
+            const float f = p.row_scale != nullptr ? p.row_scale[row] : 1.f;
+            const float v[8] = {f * lo[i].x, f * lo[i].y, f * lo[i].z, f * lo[i].w,
+                                f * hi[i].x, f * hi[i].y, f * hi[i].z, f * hi[i].w};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int n = t.nb * BN + h * 128 + lane * 4;
+              const int64_t o = row * p.out_ld + n;
+              if (p.out_vec && n + 4 <= p.N) {
+                if (p.out_f32)
+                  *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) =
+                      make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+                else
+                  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + o) =
+                      bf16x4(v + 4 * h);
+              } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  if (n + c < p.N) {
+                    if (p.out_f32) static_cast<float*>(p.out)[o + c] = v[4 * h + c];
+                    else static_cast<__nv_bfloat16*>(p.out)[o + c] = __float2bfloat16_rn(v[4 * h + c]);
+                  }
+              }
+            }
+          } else {
+            const float h[4] = {silu_f32(lo[i].x) * hi[i].x, silu_f32(lo[i].y) * hi[i].y,
+                                silu_f32(lo[i].z) * hi[i].z, silu_f32(lo[i].w) * hi[i].w};
+            const int col = t.nb * BLK + lane * 4;
+            float m = 0.f;
+            if (col < p.N)  // N is a multiple of 16
+              m = max_nan(max_nan(fabsf(h[0]), fabsf(h[1])), max_nan(fabsf(h[2]), fabsf(h[3])));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float s = block_scale(m);
+            if (col < p.N)
+              *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + row * p.out_ld + col) =
+                  encode4(h, Divisor(s));
+            if (lane == 0) p.out_scale[row * p.n_blocks + t.nb] = s;
+          }
         }
       }
     }

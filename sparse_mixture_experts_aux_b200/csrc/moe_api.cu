@@ -187,6 +187,7 @@ struct DeviceInfo {
   bool ready = false;
   int num_sms = 0;
   int pair_clusters[2] = {0, 0};  // co-resident 2-CTA clusters of each pair GEMM kernel
+  int split_clusters[9] = {};     // [s]: co-resident s-CTA clusters of the block-scaled products
 };
 constexpr int kMaxDevices = 64;
 DeviceInfo g_devices[kMaxDevices];
@@ -203,6 +204,30 @@ bool f8b_attr() {
   return cudaFuncSetAttribute(moe::f8b::gemm_kernel<MODE, SPLIT>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
                               moe::f8b::SMEM_BYTES) == cudaSuccess;
+}
+
+// Co-resident clusters of 2..8 CTAs (fewer than SMs / size where a GPC's SMs do
+// not divide: 15 of 8 on a B200).
+bool f8b_clusters(int* clusters) {
+  for (int s = 2; s <= 8; ++s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(s));
+    cfg.blockDim = dim3(moe::f8b::NUM_THREADS);
+    cfg.dynamicSmemBytes = moe::f8b::SMEM_BYTES;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(s);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, moe::f8b::gemm_kernel<moe::f8b::MATMUL, true>, &cfg) !=
+        cudaSuccess)
+      return false;
+    clusters[s] = n;
+  }
+  return true;
 }
 
 template <int EPI, int AR, bool Q8 = false>
@@ -311,7 +336,8 @@ bool pair_setup(int num_sms, int* clusters) {
   return true;
 }
 
-moe_status device_setup(int* num_sms, int* pair_clusters = nullptr) {
+moe_status device_setup(int* num_sms, int* pair_clusters = nullptr,
+                        const int** split_clusters = nullptr) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MOE_ERR_CUDA;
   std::lock_guard<std::mutex> lock(g_dev_mutex);
@@ -359,7 +385,8 @@ moe_status device_setup(int* num_sms, int* pair_clusters = nullptr) {
                              moe::rtc::SMEM_LIMIT) != cudaSuccess)
       return MOE_ERR_CUDA;
     if (!f8b_attr<moe::f8b::MATMUL, false>() || !f8b_attr<moe::f8b::MATMUL, true>() ||
-        !f8b_attr<moe::f8b::SWIGLU, false>() || !f8b_attr<moe::f8b::SWIGLU, true>())
+        !f8b_attr<moe::f8b::SWIGLU, false>() || !f8b_attr<moe::f8b::SWIGLU, true>() ||
+        !f8b_clusters(di.split_clusters))
       return MOE_ERR_CUDA;
     const int rs = static_cast<int>(moe::route_smem_bytes(moe::tc::MAX_E));
     if (cudaFuncSetAttribute(moe::route_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -370,6 +397,7 @@ moe_status device_setup(int* num_sms, int* pair_clusters = nullptr) {
     di.ready = true;
   }
   *num_sms = di.num_sms;
+  if (split_clusters != nullptr) *split_clusters = di.split_clusters;
   if (pair_clusters != nullptr) {
     pair_clusters[0] = di.pair_clusters[0];
     pair_clusters[1] = di.pair_clusters[1];
@@ -1060,10 +1088,11 @@ moe::bal::BalParams balance_params(const moe_balance_dims* d, const void* logits
 template <typename TL, bool SIG>
 void launch_balance(const moe::bal::BalParams& p, cudaStream_t st) {
   const unsigned grid = p.nchunks < 1 ? 1u : static_cast<unsigned>(p.nchunks);
-#define MOE_BAL_FWD(G, NV)                                                                  \
-  launch_pdl(moe::bal::balance_kernel<TL, G, NV, SIG, (NV > 8 ? 256 : 1024)>, grid,          \
-             (NV > 8 ? 256 : 1024),                                                          \
-             static_cast<size_t>(p.E) * 4 * ((NV > 8 ? 8 : 32) + 1), st, p)
+  // threads: the registers a row takes, and at most 48 KB of shared sums
+#define MOE_BAL_FWD(G, NV)                                                                    \
+  launch_pdl(moe::bal::balance_kernel<TL, G, NV, SIG, (NV > 8 ? 8192 / NV : 1024)>, grid,     \
+             (NV > 8 ? 8192 / NV : 1024),                                                     \
+             static_cast<size_t>(p.E) * 4 * ((NV > 8 ? 256 / NV : 32) + 1), st, p)
   MOE_BAL_DISPATCH(p.E, MOE_BAL_FWD);
 #undef MOE_BAL_FWD
   if (p.nchunks > 1)
@@ -1073,8 +1102,8 @@ void launch_balance(const moe::bal::BalParams& p, cudaStream_t st) {
 template <typename TL, bool SIG>
 void launch_balance_backward(const moe::bal::BalParams& p, const float* dloss, TL* dlogits,
                              cudaStream_t st) {
-  // a warp's run of tokens: about 16 warps an SM, at least one round of its groups
-  const int per = p.E <= 8 ? 4 : (p.E <= 16 ? 2 : 1);
+  // a warp's run of tokens: up to 32 warps an SM, whole rounds of a warp's rows
+  const int per = p.E <= 8 ? 16 : (p.E <= 16 ? 8 : (p.E <= 64 ? 4 : (p.E <= 128 ? 2 : 1)));
   int64_t run = (static_cast<int64_t>(p.T) + 148 * 32 - 1) / (148 * 32);
   run = (run + per - 1) / per * per;
   const int64_t warps = (p.T + run - 1) / run;
@@ -1109,7 +1138,7 @@ bool encode_map_codes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t 
 // N, E and M are checked. w1 is the up projection of SWIGLU.
 template <int MODE>
 moe_status launch_f8b(moe::f8b::Params& p, int K, const void* a, int64_t lda, const void* w0,
-                      const void* w1, int num_sms, cudaStream_t st) {
+                      const void* w1, int num_sms, const int* clusters, cudaStream_t st) {
   using namespace moe::f8b;
   p.k_blocks = (K + BLK - 1) / BLK;
   p.n_blocks = (p.N + BLK - 1) / BLK;
@@ -1127,15 +1156,27 @@ moe_status launch_f8b(moe::f8b::Params& p, int K, const void* a, int64_t lda, co
   if (!encode_map_codes(&maps.w0, w0, K, p.N, p.E, K, BLK) ||
       (MODE == SWIGLU && !encode_map_codes(&maps.w1, w1, K, p.N, p.E, K, BLK)))
     return MOE_ERR_CUDA;
-  // dense products of few tiles: clusters that share a tile, of the largest
-  // size that one wave holds (at least two K blocks a CTA)
+  // Clusters that share a tile where there are few: a tile then costs its share
+  // of the K blocks and about eight blocks' time of set-up and of adding up, in
+  // as many rounds as the co-resident clusters need (the persistent form sets up
+  // once). Grouped products are bounded by their largest number of tiles; what
+  // the offsets do not fill exits at once.
   const bool dense = p.offsets == nullptr && p.tile_start == nullptr;
-  const int64_t tiles = static_cast<int64_t>(p.n_tiles) * ((p.M + BM - 1) / BM);
+  const int64_t row_tiles = dense ? (p.M + BM - 1) / BM
+                                  : (p.M < p.E ? p.M : p.E) + static_cast<int64_t>(p.M) / BM;
+  const int64_t tiles = p.n_tiles * row_tiles;
   int cluster = 1;
-  if (dense)
-    while (cluster < 8 && tiles * (cluster + 1) <= num_sms && p.k_blocks >= 2 * (cluster + 1))
-      ++cluster;
-  const int64_t grid = cluster > 1 || (dense && tiles < num_sms) ? tiles * cluster : num_sms;
+  int64_t best = (tiles + num_sms - 1) / num_sms * p.k_blocks + 4;
+  for (int s = 2; s <= 8 && p.k_blocks >= 2 * s && tiles <= 4 * num_sms; ++s) {
+    if (clusters[s] < 1) continue;
+    const int64_t cost =
+        (tiles + clusters[s] - 1) / clusters[s] * ((p.k_blocks + s - 1) / s + 8);
+    if (cost < best) {
+      best = cost;
+      cluster = s;
+    }
+  }
+  const int64_t grid = cluster > 1 || tiles < num_sms ? tiles * cluster : num_sms;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(NUM_THREADS);
@@ -1186,7 +1227,8 @@ moe_status run_f8b(const moe_fp8_block_dims* d, const uint8_t* a, const float* a
       !aligned(s1, 4) || !aligned(out, two ? 16 : out_el) || !aligned(out_scale, 4))
     return MOE_ERR_INVALID_ARG;
   int num_sms = 0;
-  const moe_status ds = device_setup(&num_sms);
+  const int* clusters = nullptr;
+  const moe_status ds = device_setup(&num_sms, nullptr, &clusters);
   if (ds != MOE_OK) return ds;
   moe::f8b::Params p{};
   p.offsets = d->offsets;
@@ -1206,7 +1248,7 @@ moe_status run_f8b(const moe_fp8_block_dims* d, const uint8_t* a, const float* a
   p.timeout_ns = d->wait_timeout_ns != 0 ? static_cast<unsigned long long>(d->wait_timeout_ns)
                                          : kWaitTimeoutNs;
   p.drain_timeout_ns = kDrainTimeoutNs;
-  return launch_f8b<MODE>(p, d->K, a, d->lda != 0 ? d->lda : d->K, w0, w1, num_sms,
+  return launch_f8b<MODE>(p, d->K, a, d->lda != 0 ? d->lda : d->K, w0, w1, num_sms, clusters,
                           static_cast<cudaStream_t>(d->stream));
 }
 
