@@ -168,6 +168,20 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
  * Needs bf16 x, no shared expert, and d, d_e multiples of 256.
  */
 #define MOE_WEIGHTS_MXFP4 3
+/*
+ * Block-scaled FP8 on both GEMM operands (DeepSeek-V3's own format:
+ * jacopoparretti "Mixture of experts, token by token", "Memory"): expert weights
+ * as E4M3 codes with one fp32 scale for each 128 x 128 block, and inside the
+ * experts the token rows x and the hidden rows H (from H's fp32 value) as E4M3
+ * codes with one fp32 scale for each 128 columns of a row (the rule of
+ * moe_quantize_fp8_block). The layer runs the products below it:
+ * moe_swiglu_fp8_block's kernel for gate, up, SwiGLU and H's quantisation, then
+ * moe_matmul_fp8_block's for down, times the gates. moe_dims.weight_scales holds
+ * the block scales of the three stacks one after another: W_g [E][ceil(d_e /
+ * 128)][ceil(d / 128)], W_u the same, W_d [E][ceil(d / 128)][ceil(d_e / 128)].
+ * Needs bf16 x and no shared expert. (The values 4 and 5 name no format.)
+ */
+#define MOE_WEIGHTS_FP8_BLOCK 6
 
 typedef struct {
   int64_t T;                 /* tokens in this call (0 allowed: empty batch) */
@@ -199,11 +213,15 @@ typedef struct {
                                 MOE_WEIGHTS_FP8_W8A8 (2): the same weights, and E4M3
                                 activations inside the experts (see above);
                                 MOE_WEIGHTS_MXFP4 (3): packed E2M1 codes with block scales
-                                and row factors, see above and moe_quantize_mxfp4 */
+                                and row factors, see above and moe_quantize_mxfp4;
+                                MOE_WEIGHTS_FP8_BLOCK (6): E4M3 codes with a scale for each
+                                128 x 128 block, E4M3 activations, see above and
+                                moe_quantize_fp8_block */
   const float* weight_scales; /* MOE_WEIGHTS_FP8(_W8A8): device fp32, the per-row scales of the
                                  three stacks one after another: W_g [E*d_e], W_u [E*d_e],
                                  W_d [E*d] (what moe_quantize_fp8 writes for each stack);
-                                 MOE_WEIGHTS_MXFP4: the row factors, in the same order */
+                                 MOE_WEIGHTS_MXFP4: the row factors, in the same order;
+                                 MOE_WEIGHTS_FP8_BLOCK: the block scales, in the same order */
   uint64_t wait_timeout_ns;  /* limit of each device-side mbarrier wait in the GEMM
                                 kernels; 0 = default (4 s). A tiny value makes the waits
                                 expire on purpose: the kernels then record
@@ -230,7 +248,7 @@ MOE_API int64_t moe_capacity(int64_t T, int E, int k, float capacity_factor);
  *   x        device [T, d]            dtype
  *   W_r      device [E, d]            fp32 (the router's d x E matrix, stored expert-major)
  *   W_g, W_u device [E, d_e, d]       dtype (nn.Linear weight layout: K contiguous),
- *                                    or uint8 E4M3 codes with MOE_WEIGHTS_FP8(_W8A8)
+ *                                    or uint8 E4M3 codes with MOE_WEIGHTS_FP8(_W8A8, _BLOCK)
  *   W_d      device [E, d, d_e]       dtype (or uint8 codes)
  *   W_shared device, packed [gate (d_s x d) | up (d_s x d) | down (d x d_s)], or
  *            NULL when dims->d_s == 0
@@ -285,11 +303,14 @@ typedef struct {
   size_t yrows;       /* dtype [rows_max, d]   gate-scaled expert outputs */
   int64_t rows_max;   /* rows reserved for the permuted buffers */
   int64_t capacity;   /* C, or -1 */
-  /* MOE_WEIGHTS_FP8_W8A8 only (0 otherwise); xp then holds E4M3 codes
-   * [rows_max, d] (row stride d bytes) */
-  size_t xscale;      /* fp32 [rows_max]       scale of each permuted x row */
+  /* MOE_WEIGHTS_FP8_W8A8 and MOE_WEIGHTS_FP8_BLOCK only (0 otherwise); xp then
+   * holds E4M3 codes [rows_max, d] (row stride d bytes), and with _BLOCK there is
+   * no h */
+  size_t xscale;      /* fp32 [rows_max]       scale of each permuted x row (_BLOCK:
+                                               [rows_max, ceil(d / 128)]) */
   size_t hq;          /* uint8 [rows_max, d_e] E4M3 codes of the hidden rows */
-  size_t hscale;      /* fp32 [rows_max]       scale of each hidden row */
+  size_t hscale;      /* fp32 [rows_max]       scale of each hidden row (_BLOCK:
+                                               [rows_max, ceil(d_e / 128)]) */
   size_t status;      /* int32: this call's status word, 0 when no device-side wait of
                          this call gave up, nonzero otherwise (valid once the call's
                          stream has been synchronised; cleared at the start of each call) */

@@ -26,6 +26,7 @@ MOE_F32 = 0
 MOE_BF16 = 1
 MOE_GATE_RENORM, MOE_GATE_RAW, MOE_GATE_SIGMOID = 0, 1, 2
 MOE_WEIGHTS_DTYPE, MOE_WEIGHTS_FP8, MOE_WEIGHTS_FP8_W8A8, MOE_WEIGHTS_MXFP4 = 0, 1, 2, 3
+MOE_WEIGHTS_FP8_BLOCK = 6
 MOE_NUM_KERNELS = 7
 MOE_BALANCE_SMALL_T = 32
 KERNEL_NAMES = ("router_logits", "route", "scan", "scatter", "gate_up_swiglu", "down_scale", "combine")

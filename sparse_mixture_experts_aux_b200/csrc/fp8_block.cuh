@@ -182,6 +182,62 @@ __global__ void __launch_bounds__(256) quantize_row_blocks_kernel(
   }
 }
 
+// The layer's permute step on this format: token rows quantised in 1 x 128 blocks
+// and their codes and scales stored at each kept assignment's row (the positions
+// are those of scatter_kernel in permute.cuh). One warp a token and 512 columns:
+// eight lanes a block, sixteen elements a lane.
+template <typename TX>
+__global__ void __launch_bounds__(256) quantize_scatter_kernel(
+    const TX* __restrict__ x, int d, int T, int k, int E, int64_t C,
+    const int32_t* __restrict__ idx, const float* __restrict__ gate,
+    const int32_t* __restrict__ lrank, const int32_t* __restrict__ base,
+    const int32_t* __restrict__ tile_start, int32_t* __restrict__ slot_pos,
+    float* __restrict__ row_gate, uint8_t* __restrict__ codes, float* __restrict__ scales,
+    int64_t rows_max) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x * (blockDim.x >> 5) + warp;
+  if (t >= T) return;  // warp-uniform
+  int mypos = -1;
+  if (lane < k) {
+    const size_t a = (size_t)t * k + lane;
+    const int e = idx[a];
+    const int rank = base[(size_t)(t / ROUTE_CHUNK) * E + e] + lrank[a];
+    if (C < 0 || (int64_t)rank < C) mypos = tile_start[e] * ROW_TILE + rank;
+#if defined(MOE_DEBUG)
+    if (mypos >= 0 && ((int64_t)mypos >= rows_max || mypos >= tile_start[e + 1] * ROW_TILE ||
+                       e < 0 || e >= E)) {
+      flag_bounds();
+      mypos = -1;
+    }
+#else
+    (void)rows_max;
+#endif
+    if (blockIdx.y == 0) {
+      if (mypos >= 0) row_gate[mypos] = gate[a];
+      slot_pos[a] = mypos;
+    }
+  }
+  const int kb = (d + BLK - 1) / BLK;
+  const int c = blockIdx.y * 512 + lane * 16, b = c / BLK;
+  Vec16E<TX> v;
+  if (c < d) v.load(x + (size_t)t * d + c); else v.zero();
+  float m = v.absmax();
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float s = block_scale(m);
+  const uint4 q = v.codes(Divisor(s));
+  for (int i = 0; i < k; ++i) {
+    const int64_t row = __shfl_sync(0xffffffffu, mypos, i);
+    if (row < 0) continue;
+    if (c < d) {
+      st_v4(codes + row * d + c, q);
+      if ((lane & 7) == 0) scales[row * kb + b] = s;
+    }
+  }
+}
+
 // 128 x 128 blocks: one block of 256 threads each, 64 elements a thread; four
 // (fp32: two) blocks an SM, so that one's loads cover another's arithmetic.
 template <typename TX>

@@ -53,10 +53,11 @@ struct Plan {
   int64_t rows_max;
   size_t o_logits, o_idx, o_gate, o_lrank, o_slot, o_hist, o_base, o_psum_part, o_probsum,
       o_tile_start, o_pair_start, o_status, o_wsplit, o_rowgate, o_xp, o_h, o_yrows, o_hs, o_ys,
-      // E4M3 activations (MOE_WEIGHTS_FP8_W8A8): x codes and scales per token,
+      // E4M3 activations (MOE_WEIGHTS_FP8_W8A8 and _BLOCK): x codes and scales per token,
       // scales of the permuted x rows, H codes and scales per permuted row
       o_xq, o_sx, o_xsc, o_hq, o_hsc, total;
   bool w8a8;
+  bool fp8b;  // MOE_WEIGHTS_FP8_BLOCK
 };
 
 int64_t capacity_of(int64_t T, int E, int k, float cf) {
@@ -87,7 +88,8 @@ moe_status check_dims(const moe_dims* dims, int E, int k, float cf) {
       dims->T * static_cast<int64_t>(E) >= (int64_t(1) << 40))
     return MOE_ERR_UNSUPPORTED;
   if (dims->weight_format != MOE_WEIGHTS_DTYPE && dims->weight_format != MOE_WEIGHTS_FP8 &&
-      dims->weight_format != MOE_WEIGHTS_FP8_W8A8 && dims->weight_format != MOE_WEIGHTS_MXFP4)
+      dims->weight_format != MOE_WEIGHTS_FP8_W8A8 && dims->weight_format != MOE_WEIGHTS_MXFP4 &&
+      dims->weight_format != MOE_WEIGHTS_FP8_BLOCK)
     return MOE_ERR_INVALID_ARG;
   if (dims->weight_format != MOE_WEIGHTS_DTYPE && (dims->dtype != MOE_BF16 || dims->d_s != 0))
     return MOE_ERR_UNSUPPORTED;
@@ -164,18 +166,23 @@ Plan make_plan(const moe_dims* dims, int E, int k, float cf) {
   // tensor-core router: the hi / mid / lo bf16 terms of W_r, [3][E][d]
   p.o_wsplit = take(p.router_tc ? static_cast<size_t>(3) * E * p.d * 2 : 0);
   p.o_rowgate = take(R * 4);
-  p.o_xp = take(R * p.d * p.esz);
+  // block-scaled FP8: x and H exist as codes alone (o_xp, o_hq)
+  p.fp8b = dims->weight_format == MOE_WEIGHTS_FP8_BLOCK;
+  p.o_xp = take(R * p.d * (p.fp8b ? 1 : p.esz));
   // H: fp32 with E4M3 activations (quantised per row from its fp32 value)
-  p.o_h = take(R * p.de * (dims->weight_format == MOE_WEIGHTS_FP8_W8A8 ? 4 : p.esz));
+  p.o_h = take(p.fp8b ? 0 : R * p.de * (dims->weight_format == MOE_WEIGHTS_FP8_W8A8 ? 4 : p.esz));
   p.o_yrows = take(R * p.d * p.esz);
   p.o_hs = take(p.ds ? T * p.ds * p.esz : 0);
   p.o_ys = take(p.ds ? T * p.d * p.esz : 0);
   p.w8a8 = dims->weight_format == MOE_WEIGHTS_FP8_W8A8;
   p.o_xq = take(p.w8a8 ? T * p.d : 0);
   p.o_sx = take(p.w8a8 ? T * 4 : 0);
-  p.o_xsc = take(p.w8a8 ? R * 4 : 0);
-  p.o_hq = take(p.w8a8 ? R * p.de : 0);
-  p.o_hsc = take(p.w8a8 ? R * 4 : 0);
+  // scales of the permuted rows: one a row, or one for each 128 columns
+  const size_t kbd = p.fp8b ? (p.d + moe::f8b::BLK - 1) / moe::f8b::BLK : (p.w8a8 ? 1 : 0);
+  const size_t kbe = p.fp8b ? (p.de + moe::f8b::BLK - 1) / moe::f8b::BLK : (p.w8a8 ? 1 : 0);
+  p.o_xsc = take(R * kbd * 4);
+  p.o_hq = take(p.w8a8 || p.fp8b ? R * p.de : 0);
+  p.o_hsc = take(R * kbe * 4);
   p.total = off;
   return p;
 }
@@ -592,6 +599,11 @@ moe_status launch_route_and_permute(const Plan& P, const moe_dims* dims, const T
       dim3 qgrid((T + 7) / 8, (qvec + moe::PERMUTE_CHUNK_VECS - 1) / moe::PERMUTE_CHUNK_VECS);
       launch_pdl(moe::scatter_kernel<uint8_t>, qgrid, 256, 0, st, xq, P.d, T, P.k, P.E, P.C, idx, gate, lrank, base, tile_start, slot, rowgate,
           reinterpret_cast<uint8_t*>(xp), P.rows_max, sx, reinterpret_cast<float*>(ws + P.o_xsc));
+    } else if (P.fp8b) {
+      dim3 qgrid((T + 7) / 8, (P.d + 511) / 512);
+      launch_pdl(moe::f8b::quantize_scatter_kernel<TX>, qgrid, 256, 0, st, x, P.d, T, P.k, P.E, P.C, idx,
+                 gate, lrank, base, tile_start, slot, rowgate, reinterpret_cast<uint8_t*>(xp),
+                 reinterpret_cast<float*>(ws + P.o_xsc), P.rows_max);
     } else if (dims->weight_format == MOE_WEIGHTS_FP8 || dims->weight_format == MOE_WEIGHTS_MXFP4) {
       // the quantised-weight GEMMs read fp16 rows
       launch_pdl(moe::scatter_kernel<TX, true>, grid, 256, 0, st, x, P.d, T, P.k, P.E, P.C, idx, gate,
@@ -603,6 +615,87 @@ moe_status launch_route_and_permute(const Plan& P, const moe_dims* dims, const T
                                                     P.rows_max, nullptr, nullptr);
   }
   tm.at(7);
+  return launched();
+}
+
+// ---------------------------------------------------------------------------
+// Block-scaled FP8 products (fp8_block_gemm.cuh).
+// ---------------------------------------------------------------------------
+
+// Tensor map over codes [outer][rows][cols] (cols a multiple of 16, rows `ld`
+// bytes apart), box {128 bytes, box_rows, 1}, 128-byte swizzle; described as
+// 32-bit words. Everything outside reads as zero.
+bool encode_map_codes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
+                      uint64_t outer, uint64_t ld, uint32_t box_rows) {
+  cuuint64_t dims[3] = {cols / 4, rows, outer};
+  cuuint64_t strides[2] = {ld, ld * rows};
+  cuuint32_t box[3] = {moe::f8b::BLK / 4, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One product: p holds the operands' scales, the segments and the outputs; K,
+// N, E and M are checked. w1 is the up projection of SWIGLU. At most `rows` of the
+// M rows of A belong to an expert.
+template <int MODE>
+moe_status launch_f8b(moe::f8b::Params& p, int64_t rows, int K, const void* a, int64_t lda, const void* w0,
+                      const void* w1, int num_sms, const int* clusters, cudaStream_t st) {
+  using namespace moe::f8b;
+  p.k_blocks = (K + BLK - 1) / BLK;
+  p.n_blocks = (p.N + BLK - 1) / BLK;
+  p.n_tiles = MODE == SWIGLU ? p.n_blocks : (p.n_blocks + 1) / 2;
+  // the kernels count tiles in 32 bits
+  if ((static_cast<int64_t>(p.M) / BM + p.E + 1) * p.n_tiles >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  Maps maps;
+  memset(&maps, 0, sizeof(maps));
+  const uint32_t boxes[A_BOXES] = {16, 64, 128};
+  for (int i = 0; i < A_BOXES; ++i)
+    if (!encode_map_codes(&maps.a[i], a, K, p.M, 1, lda, boxes[i])) return MOE_ERR_CUDA;
+  if (!encode_map_codes(&maps.w0, w0, K, p.N, p.E, K, BLK)) return MOE_ERR_CUDA;
+  if (MODE == SWIGLU && !encode_map_codes(&maps.w1, w1, K, p.N, p.E, K, BLK)) return MOE_ERR_CUDA;
+  if (!encode_map_codes(&maps.w0, w0, K, p.N, p.E, K, BLK) ||
+      (MODE == SWIGLU && !encode_map_codes(&maps.w1, w1, K, p.N, p.E, K, BLK)))
+    return MOE_ERR_CUDA;
+  // Clusters that share a tile where there are few: a tile then costs its share
+  // of the K blocks and about eight blocks' time of set-up and of adding up, in
+  // as many rounds as the co-resident clusters need (the persistent form sets up
+  // once). Grouped products are bounded by their largest number of tiles; what
+  // the offsets do not fill exits at once.
+  const bool dense = p.offsets == nullptr && p.tile_start == nullptr;
+  const int64_t row_tiles = dense ? (rows + BM - 1) / BM : (rows < p.E ? rows : p.E) + rows / BM;
+  const int64_t tiles = p.n_tiles * row_tiles;
+  int cluster = 1;
+  int64_t best = (tiles + num_sms - 1) / num_sms * p.k_blocks + 4;
+  for (int s = 2; s <= 8 && p.k_blocks >= 2 * s && tiles <= 4 * num_sms; ++s) {
+    if (clusters[s] < 1) continue;
+    const int64_t cost =
+        (tiles + clusters[s] - 1) / clusters[s] * ((p.k_blocks + s - 1) / s + 8);
+    if (cost < best) {
+      best = cost;
+      cluster = s;
+    }
+  }
+  const int64_t grid = cluster > 1 || tiles < num_sms ? tiles * cluster : num_sms;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  (void)(cluster > 1 ? cudaLaunchKernelEx(&cfg, gemm_kernel<MODE, true>, maps, p)
+                     : cudaLaunchKernelEx(&cfg, gemm_kernel<MODE, false>, maps, p));
   return launched();
 }
 
@@ -642,7 +735,8 @@ moe_status forward_impl(const moe_dims* dims, const void* x, const float* W_r, c
       dims->workspace_bytes < P.total)
     return MOE_ERR_WORKSPACE;
   int num_sms = 0, pair_clusters[2] = {0, 0};
-  s = device_setup(&num_sms, pair_clusters);
+  const int* split_clusters = nullptr;
+  s = device_setup(&num_sms, pair_clusters, &split_clusters);
   if (s != MOE_OK) return s;
 
   uint8_t* ws = static_cast<uint8_t*>(dims->workspace);
@@ -671,7 +765,48 @@ moe_status forward_impl(const moe_dims* dims, const void* x, const float* W_r, c
     const size_t sh_n = static_cast<size_t>(P.ds) * P.d;
     const int ng = P.ds ? 2 : 1;
 
-    if (P.w8a8) {
+    if (P.fp8b) {
+      // block-scaled FP8: gate/up with SwiGLU and H's quantisation in one kernel,
+      // then the down product with the gates (fp8_block_gemm.cuh)
+      uint8_t* hq = ws + P.o_hq;
+      float* hsc = reinterpret_cast<float*>(ws + P.o_hsc);
+      const int64_t kbd = (P.d + moe::f8b::BLK - 1) / moe::f8b::BLK;
+      const int64_t kbe = (P.de + moe::f8b::BLK - 1) / moe::f8b::BLK;
+      moe::f8b::Params up{};
+      up.tile_start = tile_start;
+      up.counts = counts;
+      up.cap = P.C;
+      up.E = E;
+      up.M = rows_cap;
+      up.timeout_ns = wait_tmo;
+      up.drain_timeout_ns = kDrainTimeoutNs;
+      up.call_err = call_err;
+      moe::f8b::Params dn = up;
+      up.N = P.de;
+      up.a_scale = reinterpret_cast<const float*>(ws + P.o_xsc);
+      up.w_scale0 = dims->weight_scales;
+      up.w_scale1 = up.w_scale0 + E * kbe * kbd;
+      up.out = hq;
+      up.out_ld = P.de;
+      up.out_scale = hsc;
+      dn.N = P.d;
+      dn.a_scale = hsc;
+      dn.w_scale0 = up.w_scale1 + E * kbe * kbd;
+      dn.row_scale = rowgate;
+      dn.out = yrows;
+      dn.out_ld = P.d;
+      dn.out_vec = 1;  // d is a multiple of 64
+      tm.at(8);
+      s = launch_f8b<moe::f8b::SWIGLU>(up, P.T * P.k, P.d, xp, P.d, W_g, W_u, num_sms,
+                                       split_clusters, st);
+      tm.at(9);
+      if (s != MOE_OK) return s;
+      tm.at(10);
+      s = launch_f8b<moe::f8b::MATMUL>(dn, P.T * P.k, P.de, hq, P.de, W_d, nullptr, num_sms,
+                                       split_clusters, st);
+      tm.at(11);
+      if (s != MOE_OK) return s;
+    } else if (P.w8a8) {
       // E4M3 x E4M3 (kind::f8f6f4) on the 1-CTA kernels; H is quantised per row
       // between the two GEMMs
       const int arows = P.T <= 32 ? 32 : (P.T <= 64 ? 64 : 128);
@@ -1115,87 +1250,6 @@ void launch_balance_backward(const moe::bal::BalParams& p, const float* dloss, T
 #undef MOE_BAL_BWD
 }
 
-// ---------------------------------------------------------------------------
-// Block-scaled FP8 products (fp8_block_gemm.cuh).
-// ---------------------------------------------------------------------------
-
-// Tensor map over codes [outer][rows][cols] (cols a multiple of 16, rows `ld`
-// bytes apart), box {128 bytes, box_rows, 1}, 128-byte swizzle; described as
-// 32-bit words. Everything outside reads as zero.
-bool encode_map_codes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
-                      uint64_t outer, uint64_t ld, uint32_t box_rows) {
-  cuuint64_t dims[3] = {cols / 4, rows, outer};
-  cuuint64_t strides[2] = {ld, ld * rows};
-  cuuint32_t box[3] = {moe::f8b::BLK / 4, box_rows, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box,
-                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// One product: p holds the operands' scales, the segments and the outputs; K,
-// N, E and M are checked. w1 is the up projection of SWIGLU.
-template <int MODE>
-moe_status launch_f8b(moe::f8b::Params& p, int K, const void* a, int64_t lda, const void* w0,
-                      const void* w1, int num_sms, const int* clusters, cudaStream_t st) {
-  using namespace moe::f8b;
-  p.k_blocks = (K + BLK - 1) / BLK;
-  p.n_blocks = (p.N + BLK - 1) / BLK;
-  p.n_tiles = MODE == SWIGLU ? p.n_blocks : (p.n_blocks + 1) / 2;
-  // the kernels count tiles in 32 bits
-  if ((static_cast<int64_t>(p.M) / BM + p.E + 1) * p.n_tiles >= (int64_t(1) << 31))
-    return MOE_ERR_UNSUPPORTED;
-  Maps maps;
-  memset(&maps, 0, sizeof(maps));
-  const uint32_t boxes[A_BOXES] = {16, 64, 128};
-  for (int i = 0; i < A_BOXES; ++i)
-    if (!encode_map_codes(&maps.a[i], a, K, p.M, 1, lda, boxes[i])) return MOE_ERR_CUDA;
-  if (!encode_map_codes(&maps.w0, w0, K, p.N, p.E, K, BLK)) return MOE_ERR_CUDA;
-  if (MODE == SWIGLU && !encode_map_codes(&maps.w1, w1, K, p.N, p.E, K, BLK)) return MOE_ERR_CUDA;
-  if (!encode_map_codes(&maps.w0, w0, K, p.N, p.E, K, BLK) ||
-      (MODE == SWIGLU && !encode_map_codes(&maps.w1, w1, K, p.N, p.E, K, BLK)))
-    return MOE_ERR_CUDA;
-  // Clusters that share a tile where there are few: a tile then costs its share
-  // of the K blocks and about eight blocks' time of set-up and of adding up, in
-  // as many rounds as the co-resident clusters need (the persistent form sets up
-  // once). Grouped products are bounded by their largest number of tiles; what
-  // the offsets do not fill exits at once.
-  const bool dense = p.offsets == nullptr && p.tile_start == nullptr;
-  const int64_t row_tiles = dense ? (p.M + BM - 1) / BM
-                                  : (p.M < p.E ? p.M : p.E) + static_cast<int64_t>(p.M) / BM;
-  const int64_t tiles = p.n_tiles * row_tiles;
-  int cluster = 1;
-  int64_t best = (tiles + num_sms - 1) / num_sms * p.k_blocks + 4;
-  for (int s = 2; s <= 8 && p.k_blocks >= 2 * s && tiles <= 4 * num_sms; ++s) {
-    if (clusters[s] < 1) continue;
-    const int64_t cost =
-        (tiles + clusters[s] - 1) / clusters[s] * ((p.k_blocks + s - 1) / s + 8);
-    if (cost < best) {
-      best = cost;
-      cluster = s;
-    }
-  }
-  const int64_t grid = cluster > 1 || tiles < num_sms ? tiles * cluster : num_sms;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(NUM_THREADS);
-  cfg.dynamicSmemBytes = SMEM_BYTES;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  (void)(cluster > 1 ? cudaLaunchKernelEx(&cfg, gemm_kernel<MODE, true>, maps, p)
-                     : cudaLaunchKernelEx(&cfg, gemm_kernel<MODE, false>, maps, p));
-  return launched();
-}
-
 moe_status check_f8b(const moe_fp8_block_dims* d, bool swiglu) {
   if (d == nullptr || d->M < 0 || d->N < 1 || d->K < 16 || d->E < 0 || d->K % 16 != 0 ||
       (d->E > 0) != (d->offsets != nullptr) || !aligned(d->offsets, 4) ||
@@ -1248,7 +1302,7 @@ moe_status run_f8b(const moe_fp8_block_dims* d, const uint8_t* a, const float* a
   p.timeout_ns = d->wait_timeout_ns != 0 ? static_cast<unsigned long long>(d->wait_timeout_ns)
                                          : kWaitTimeoutNs;
   p.drain_timeout_ns = kDrainTimeoutNs;
-  return launch_f8b<MODE>(p, d->K, a, d->lda != 0 ? d->lda : d->K, w0, w1, num_sms, clusters,
+  return launch_f8b<MODE>(p, d->M, d->K, a, d->lda != 0 ? d->lda : d->K, w0, w1, num_sms, clusters,
                           static_cast<cudaStream_t>(d->stream));
 }
 

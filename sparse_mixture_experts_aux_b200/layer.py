@@ -32,7 +32,7 @@ class Workspace:
 
 def _dims_for(x: torch.Tensor, W_g: torch.Tensor, d_s: int, router_bias, ws, stream, events,
               wait_timeout_ns: int = 0, routing: Optional[dict] = None, weight_scales=None,
-              act_fp8: bool = False, weight_block_scales=None):
+              act_fp8: bool = False, weight_block_scales=None, fp8_block: bool = False):
     T, d = x.shape
     d_e = W_g.shape[1]
     routing = routing or {}
@@ -41,6 +41,8 @@ def _dims_for(x: torch.Tensor, W_g: torch.Tensor, d_s: int, router_bias, ws, str
         fmt = _lib.MOE_WEIGHTS_FP8_W8A8 if act_fp8 else _lib.MOE_WEIGHTS_FP8
         if weight_block_scales is not None:
             fmt = _lib.MOE_WEIGHTS_MXFP4
+        if fp8_block:
+            fmt = _lib.MOE_WEIGHTS_FP8_BLOCK
     return _lib.make_dims(T, d, d_e, d_s, dtype_code(x.dtype), router_bias, ws,
                           ws.numel() if ws is not None else 0, stream, events,
                           wait_timeout_ns=wait_timeout_ns,
@@ -60,7 +62,8 @@ def forward(x: torch.Tensor, W_r: torch.Tensor, W_g: torch.Tensor, W_u: torch.Te
             counts: Optional[torch.Tensor] = None, wait_timeout_ns: int = 0,
             gate_mode: int = 0, selection_bias: Optional[torch.Tensor] = None,
             n_group: int = 0, topk_group: int = 0, weight_scales: Optional[torch.Tensor] = None,
-            act_fp8: bool = False, weight_block_scales: Optional[torch.Tensor] = None):
+            act_fp8: bool = False, weight_block_scales: Optional[torch.Tensor] = None,
+            fp8_block: bool = False):
     """Run the routed MoE FFN layer; returns (y, aux[1] fp32, counts[E] int32) on x's device.
 
     Shapes: x [T, d]; W_r [E, d] fp32; W_g, W_u [E, d_e, d]; W_d [E, d, d_e];
@@ -72,6 +75,10 @@ def forward(x: torch.Tensor, W_r: torch.Tensor, W_g: torch.Tensor, W_u: torch.Te
     MXFP4 expert weights: W_g, W_u, W_d as packed uint8 E2M1 codes [.., K / 2]
     (quantize_mxfp4), weight_block_scales = their E8M0 block scales and
     weight_scales = their row factors, each concatenated [W_g | W_u | W_d].
+    Block-scaled FP8 experts (fp8_block=True, MOE_WEIGHTS_FP8_BLOCK): W_g, W_u, W_d
+    as uint8 E4M3 codes and weight_scales = their 128 x 128 block scales
+    (quantize_fp8_block), concatenated [W_g | W_u | W_d]; E4M3 activations with a
+    scale for each 128 columns inside the experts.
     wait_timeout_ns: limit of the GEMM kernels' device-side waits (0 = library default).
     gate_mode / selection_bias / n_group / topk_group: routing variants (include/moe.h).
     """
@@ -96,15 +103,21 @@ def forward(x: torch.Tensor, W_r: torch.Tensor, W_g: torch.Tensor, W_u: torch.Te
         raise RuntimeError("act_fp8 needs FP8 (uint8) weights")
     if weight_block_scales is not None and (act_fp8 or W_g.dtype != torch.uint8):
         raise RuntimeError("weight_block_scales go with MXFP4 (uint8) weights, without act_fp8")
+    if fp8_block:
+        if W_g.dtype != torch.uint8 or act_fp8 or weight_block_scales is not None:
+            raise RuntimeError("fp8_block needs uint8 weights, without act_fp8 or weight_block_scales")
+        blocks = 3 * E * (-(-x.shape[1] // 128)) * (-(-W_g.shape[1] // 128))
+        if weight_scales.numel() != blocks or not weight_scales.is_contiguous():
+            raise RuntimeError(f"fp8_block needs {blocks} weight_scales, one after another")
     probe = _dims_for(x, W_g, d_s, router_bias, None, stream, events, routing=routing,
                       weight_scales=weight_scales, act_fp8=act_fp8,
-                      weight_block_scales=weight_block_scales)
+                      weight_block_scales=weight_block_scales, fp8_block=fp8_block)
     nbytes = _lib.moe_workspace_size(probe, E, k, capacity_factor)
     if nbytes == 0:
         raise _lib.MoeError(_lib.MOE_ERR_INVALID_ARG, "moe_workspace_size")
     ws = workspace.get(nbytes, dev)
     dims = _dims_for(x, W_g, d_s, router_bias, ws, stream, events, wait_timeout_ns, routing,
-                     weight_scales, act_fp8, weight_block_scales)
+                     weight_scales, act_fp8, weight_block_scales, fp8_block)
     y = torch.empty_like(x) if y is None else y
     aux = torch.empty(1, dtype=torch.float32, device=dev) if aux is None else aux
     counts = torch.empty(E, dtype=torch.int32, device=dev) if counts is None else counts
@@ -173,11 +186,13 @@ def dequantize_mxfp4(codes: torch.Tensor, bscales: torch.Tensor, factors: torch.
 
 
 def routing_views(ws: torch.Tensor, x: torch.Tensor, W_g: torch.Tensor, E: int, k: int,
-                  capacity_factor: float = 0.0, d_s: int = 0, act_fp8: bool = False) -> dict:
+                  capacity_factor: float = 0.0, d_s: int = 0, act_fp8: bool = False,
+                  fp8_block: bool = False) -> dict:
     """Views of the routing results moe_forward left in workspace `ws` (with
-    act_fp8 and FP8 weights, also the E4M3 activation rows and their scales)."""
+    act_fp8 or fp8_block and FP8 weights, also the E4M3 activation rows and their
+    scales; with fp8_block these stand in the place of xp and h)."""
     T, d = x.shape
-    dims = _dims_for(x, W_g, d_s, None, ws, 0, None, act_fp8=act_fp8)
+    dims = _dims_for(x, W_g, d_s, None, ws, 0, None, act_fp8=act_fp8, fp8_block=fp8_block)
     L = _lib.moe_workspace_layout(dims, E, k, capacity_factor)
     b = ws
 
@@ -193,8 +208,9 @@ def routing_views(ws: torch.Tensor, x: torch.Tensor, W_g: torch.Tensor, E: int, 
         slot_pos=view(L.slot_pos, T * k, torch.int32).view(T, k),
         probsum=view(L.probsum, E, torch.float64),
         tile_start=view(L.tile_start, E + 1, torch.int32),
-        xp=view(L.xp, L.rows_max * d, x.dtype).view(L.rows_max, d),
-        h=view(L.h, L.rows_max * d_e, x.dtype).view(L.rows_max, d_e),
+        **({} if fp8_block else dict(
+            xp=view(L.xp, L.rows_max * d, x.dtype).view(L.rows_max, d),
+            h=view(L.h, L.rows_max * d_e, x.dtype).view(L.rows_max, d_e))),
         yrows=view(L.yrows, L.rows_max * d, x.dtype).view(L.rows_max, d),
         rows_max=L.rows_max, capacity=L.capacity,
         status=view(L.status, 1, torch.int32),
@@ -202,4 +218,9 @@ def routing_views(ws: torch.Tensor, x: torch.Tensor, W_g: torch.Tensor, E: int, 
                 xscale=view(L.xscale, L.rows_max, torch.float32),
                 hq=view(L.hq, L.rows_max * d_e, torch.uint8).view(L.rows_max, d_e),
                 hscale=view(L.hscale, L.rows_max, torch.float32)) if act_fp8 else {}),
+        **(dict(xq=view(L.xp, L.rows_max * d, torch.uint8).view(L.rows_max, d),
+                xscale=view(L.xscale, L.rows_max * -(-d // 128), torch.float32).view(L.rows_max, -1),
+                hq=view(L.hq, L.rows_max * d_e, torch.uint8).view(L.rows_max, d_e),
+                hscale=view(L.hscale, L.rows_max * -(-d_e // 128), torch.float32).view(L.rows_max, -1))
+           if fp8_block else {}),
     )

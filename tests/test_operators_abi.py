@@ -123,3 +123,23 @@ def test_product_pointers():
 def test_product_of_no_rows():
     assert _lib.moe_matmul_fp8_block(product(M=0), 0, 0, 0, 0, 0) == _lib.MOE_OK
     assert _lib.moe_swiglu_fp8_block(product(M=0), 0, 0, 0, 0, 0, 0, 0, 0) == _lib.MOE_OK
+
+
+def test_layer_format():
+    def dims(**kw):
+        base = dict(T=128, d=256, d_e=320, dtype=_lib.MOE_BF16,
+                    weight_format=_lib.MOE_WEIGHTS_FP8_BLOCK)
+        return _lib.make_dims(**dict(base, **kw))
+
+    need = _lib.moe_workspace_size(dims(), 8, 2, 0.0)
+    assert 0 < need < _lib.moe_workspace_size(dims(weight_format=0), 8, 2, 0.0)
+    L = _lib.moe_workspace_layout(dims(), 8, 2, 0.0)
+    assert max(L.xscale, L.hq, L.hscale) < need
+    assert L.hq - L.xscale >= L.rows_max * 2 * 4          # ceil(256 / 128) scales a row
+    assert need - L.hscale >= L.rows_max * 3 * 4          # ceil(320 / 128)
+    for kw in (dict(d_s=128), dict(dtype=_lib.MOE_F32), dict(d=288)):
+        st = _lib.moe_forward(dims(**kw), P, P, P, P, P, None, 8, 2, 0.0, P, P, P, check=False)
+        assert st == UNSUPPORTED
+    st = _lib.moe_forward(dims(workspace=P, workspace_bytes=need), P, P, P, P, P, None, 8, 2, 0.0, P,
+                          P, P, check=False)
+    assert st == BAD                                      # no weight_scales
