@@ -158,15 +158,16 @@ __device__ __forceinline__ void load_row(const TL* row, bool ok, int sub, int E,
 
 // Deterministic block sum of a double (all threads get it); red holds 32.
 __device__ __forceinline__ double block_sum(double v, double* red) {
+  const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[warp] = v;
   __syncthreads();
-  double t = 0.0;
-  for (int w = 0; w < nw; ++w) t += red[w];
-  return t;
+  v = (int)(threadIdx.x & 31) < nw ? red[threadIdx.x & 31] : 0.0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
 // L = E sum_i c_i psum_i / (n^2 k) from a block-wide sum of c_i psum_i.
@@ -180,12 +181,13 @@ __device__ __forceinline__ float loss_of(double dot, int n, int E, int k) {
 // its sums in slot (chunk + sequence), which no other pair has, or, when the
 // sequence lies inside the chunk, its results at once.
 // Dynamic shared memory: float psum[warps][E], int32 counts[E].
-template <typename TL, int G, int NV, bool SIG, int THREADS>
-__global__ void __launch_bounds__(THREADS) balance_kernel(const BalParams p) {
+template <typename TL, int G, int NV, bool SIG>
+__global__ void __launch_bounds__(NV > 8 ? 8192 / NV : 1024) balance_kernel(const BalParams p) {
   pdl_wait();
   pdl_launch_dependents();
   extern __shared__ __align__(16) uint8_t bal_smem[];
-  constexpr int WARPS = THREADS / 32, U = ROWS_AT_ONCE<NV>, PER = 32 / G * U;
+  constexpr int U = ROWS_AT_ONCE<NV>, PER = 32 / G * U;
+  const int THREADS = blockDim.x, WARPS = THREADS / 32;
   float* s_psum = reinterpret_cast<float*>(bal_smem);
   int32_t* s_cnt = reinterpret_cast<int32_t*>(s_psum + (size_t)WARPS * p.E);
   __shared__ double s_red[32];
@@ -196,14 +198,12 @@ __global__ void __launch_bounds__(THREADS) balance_kernel(const BalParams p) {
   const int c0 = blockIdx.x * p.chunk;
   const int c1 = min(p.T, c0 + p.chunk);
   if (p.nchunks == 1 && (p.cu != nullptr || p.T == 0)) {  // empty sequences: no other kernel sees them
-    for (int i = threadIdx.x; i < p.S * p.E; i += THREADS) {
-      const int s = i / p.E;
-      if (seq_begin(p.cu, s, p.T) >= seq_end(p.cu, s, p.T)) {
-        p.counts[i] = 0;
-        if (i == s * p.E) {
-          p.tokens[s] = 0;
-          p.loss[s] = 0.f;
-        }
+    for (int s = warp; s < p.S; s += WARPS) {
+      if (seq_begin(p.cu, s, p.T) < seq_end(p.cu, s, p.T)) continue;
+      for (int i = lane; i < p.E; i += 32) p.counts[(size_t)s * p.E + i] = 0;
+      if (lane == 0) {
+        p.tokens[s] = 0;
+        p.loss[s] = 0.f;
       }
     }
   }
@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(THREADS) balance_kernel(const BalParams p) {
     double dot = 0.0;
     for (int i = threadIdx.x; i < p.E; i += THREADS) {
       double acc = 0.0;
+#pragma unroll 8
       for (int w = 0; w < WARPS; ++w) acc += (double)s_psum[(size_t)w * p.E + i];
       const int c = s_cnt[i];
       if (whole) {
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(THREADS) balance_kernel(const BalParams p) {
   }
 }
 
-// One block of 1024 threads per sequence: those that met several chunks add
+// One block per sequence: those that met several chunks add
 // their slots up, empty ones get zeros. A thread per expert (rounded up to a
 // warp) and part of the slots; the parts are added in order.
 __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalParams p) {
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(1024) balance_finish_kernel(const BalParams p)
   const bool empty = qb >= qe;
   const int f = empty ? 0 : qb / p.chunk, l = empty ? -1 : (qe - 1) / p.chunk;
   if (!empty && f == l) return;  // finished where it was read
-  const int width = (p.E + 31) & ~31, parts = 1024 / width;
+  const int width = (p.E + 31) & ~31, parts = blockDim.x / width;
   const int e = threadIdx.x % width, part = threadIdx.x / width;
   double ps = 0.0;
   int c = 0;

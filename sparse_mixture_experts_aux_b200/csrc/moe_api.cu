@@ -1223,15 +1223,20 @@ moe::bal::BalParams balance_params(const moe_balance_dims* d, const void* logits
 template <typename TL, bool SIG>
 void launch_balance(const moe::bal::BalParams& p, cudaStream_t st) {
   const unsigned grid = p.nchunks < 1 ? 1u : static_cast<unsigned>(p.nchunks);
-  // threads: the registers a row takes, and at most 48 KB of shared sums
-#define MOE_BAL_FWD(G, NV)                                                                    \
-  launch_pdl(moe::bal::balance_kernel<TL, G, NV, SIG, (NV > 8 ? 8192 / NV : 1024)>, grid,     \
-             (NV > 8 ? 8192 / NV : 1024),                                                     \
-             static_cast<size_t>(p.E) * 4 * ((NV > 8 ? 256 / NV : 32) + 1), st, p)
+  // threads: what the registers of a row allow, at most 48 KB of shared sums; a
+  // chunk of 32 rows is eight warps' work, and fewer warps add up sooner
+#define MOE_BAL_FWD(G, NV)                                                                   \
+  do {                                                                                       \
+    const unsigned most = NV > 8 ? 8192 / NV : 1024;                                         \
+    const unsigned threads = p.chunk <= MOE_BALANCE_SMALL_T ? 256 : most;                    \
+    launch_pdl(moe::bal::balance_kernel<TL, G, NV, SIG>, grid, threads,                      \
+               static_cast<size_t>(p.E) * 4 * (threads / 32 + 1), st, p);                    \
+  } while (0)
   MOE_BAL_DISPATCH(p.E, MOE_BAL_FWD);
 #undef MOE_BAL_FWD
   if (p.nchunks > 1)
-    launch_pdl(moe::bal::balance_finish_kernel, static_cast<unsigned>(p.S), 1024, 0, st, p);
+    launch_pdl(moe::bal::balance_finish_kernel, static_cast<unsigned>(p.S),
+               p.E <= 64 ? 256 : 1024, 0, st, p);
 }
 
 template <typename TL, bool SIG>
