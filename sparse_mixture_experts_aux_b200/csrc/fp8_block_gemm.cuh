@@ -650,7 +650,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         mx[half * BM + r_in_tile] = m;
         asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
         m = max_nan(m, mx[(half ^ 1) * BM + r_in_tile]);
-        const float s = block_scale(m);
+        // rows behind the end hold anything: a scale of 1 keeps their lanes off the
+        // division path, which the whole warp would walk with them (64 rows over 8
+        // experts: 212 -> 182 us)
+        const float s = row_ok ? block_scale(m) : 1.f;
         const Divisor d(s);
         uint4 v[4];
 #pragma unroll
