@@ -12,7 +12,9 @@
 // gradient flows through P alone: f is a count); AI Engineering Illustrated,
 // "Fix 1" and the sequence-level loss of DeepSeek-V3.
 //
-// Bound: memory. The forward pass reads the logits once, the gradient reads
+// Bound: memory in principle (15 us for 32768 rows of 256 experts, both ways),
+// in fact the instructions of a row and the three launches: 37 us. The forward
+// pass reads the logits once, the gradient reads
 // them once more and writes as much (it needs f, a count over the whole
 // sequence). A row's softmax stays in the registers of one group of lanes.
 // Determinism: every sum has a fixed order (lane, then warp, then chunk);

@@ -6,8 +6,10 @@
 // token", "Memory".) A block that holds a NaN comes out as NaN; one that holds
 // an infinity has an infinite scale, finite elements 0 and infinite ones NaN.
 //
-// Bound: memory (bf16: 3 bytes an element, read and written once). The block
-// stays in registers between its maximum and its codes. The quotient is the
+// Bound: memory (bf16: 3 bytes an element, read and written once), close to
+// issue: 8192 x 7168 rows 33 us (5.3 TB/s, 0.81 of the measured copy), weights
+// 8 x 14336 x 4096 239 us (5.9 TB/s, 0.90). The block stays in registers between
+// its maximum and its codes. The quotient is the
 // one of an fp32 division: q = x y corrected once by its remainder,
 // q + (x - q scale) y with y = 1 / scale (Markstein, "Computation of elementary
 // functions on the IBM RISC System/6000 processor", 1990), three fused

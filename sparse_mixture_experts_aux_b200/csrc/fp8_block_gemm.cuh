@@ -23,14 +23,24 @@
 // issuer, warp 3 brings the scales and the tile's place, four K blocks at a time,
 // into a ring in shared memory, warps 4..11 epilogue (warp w reads TMEM lanes
 // 32 (w % 4)..+31, the two warps of a quadrant take 64 columns of each half of
-// the tile). The
-// epilogue threads hold 128 accumulators and two pieces of 32 partial sums, so
-// the first warpgroup hands registers to them (setmaxnreg): 4 x 32 x 56 +
-// 8 x 32 x 224 = 64512, the 384 x 168 at launch.
+// the tile). The epilogue threads hold 128 accumulators and two pieces of 32
+// partial sums, so the first warpgroup hands registers to them (setmaxnreg):
+// 4 x 32 x 56 + 8 x 32 x 224 = 64512, the 384 x 168 at launch.
 //
 // The epilogue warps touch no global memory inside the K loop: with their scales
 // loaded by themselves, the wait for a TMEM read also waited for those loads in
-// some builds and not in others (8192^2 x 4096: 1.2 to 2.1 PFLOP/s by chance).
+// some builds and not in others (4736 x 4096 x 8192: 157 to 242 us by chance).
+//
+// Bound. Many rows: the way round between the MMAs of a block (512 cycles) and
+// the epilogue's reads of it, about 860 cycles a block with the tensor pipe 53%
+// active: 4736 x 4096 x 8192 in 134 to 150 us (2.1 to 2.4 PFLOP/s) from a cool
+// start; back to back the power cap sets 1.6 to 1.7 PFLOP/s (8 experts' gate and
+// up over 8192 rows, 4096 -> 14336: 1180 us). Few rows: HBM; the same experts
+// over 64 rows 160 us in the layer, 5.9 TB/s, 0.90 of the measured copy. Not
+// kept, as slower: CTA pairs (tcgen05 cta_group::2; 171 us where this form takes
+// 150), four TMEM buffers of 128 columns (173), loading a block's first columns
+// while the last block is added (169), a ring of five or six stages for few rows
+// (182 -> 189).
 //
 // Tiles of 128 rows never straddle two experts; rows of a tile behind its
 // expert's last row are computed from whatever lies there and not stored (a
