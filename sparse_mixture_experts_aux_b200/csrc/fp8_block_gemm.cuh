@@ -72,6 +72,8 @@ constexpr int BAR_BYTES = 256;
 constexpr int SEG_BYTES = 4 * (tc::MAX_E + 1);
 constexpr int GROUP = 4;         // K blocks whose scales travel together
 constexpr int SCALE_SLOTS = 4;   // groups in flight
+constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * SCALE_SLOTS + 4;
+static_assert(8 * NUM_BARS + 8 <= BAR_BYTES, "barriers, TMEM address, abort flag");
 struct ScaleSlot {
   float a[GROUP][BM];            // the rows' scales
   float2 w[GROUP];               // the weight scales of the tile's two halves
@@ -352,8 +354,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* staging = smem + RING_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(staging + STAGING_BYTES);
   // bars: full[STAGES], empty[STAGES], tfull[2], tempty[2], done, sfull[SCALE_SLOTS],
-  // sempty[SCALE_SLOTS]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5 + 2 * SCALE_SLOTS);
+  // sempty[SCALE_SLOTS], maxima[4]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   ScaleSlot* slots = reinterpret_cast<ScaleSlot*>(staging + STAGING_BYTES + BAR_BYTES);
   int32_t* s_mt = reinterpret_cast<int32_t*>(slots + SCALE_SLOTS);
@@ -371,6 +373,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t done_bar = bar0 + 8u * (2 * STAGES + 4);
   auto sfull_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + s); };
   auto sempty_bar = [&](int s) { return bar0 + 8u * (2 * STAGES + 5 + SCALE_SLOTS + s); };
+  auto maxima_bar = [&](int quad) { return bar0 + 8u * (2 * STAGES + 5 + 2 * SCALE_SLOTS + quad); };
   uint32_t rank = 0, ranks = 1;  // SPLIT: in the cluster
   if (SPLIT) {
     rank = tc2::cluster_ctarank();
@@ -391,6 +394,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc::mbar_init(sfull_bar(s), 1);
       tc::mbar_init(sempty_bar(s), EPI_WARPS);
     }
+    for (int q = 0; q < 4; ++q) tc::mbar_init(maxima_bar(q), 2);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     for (int b = 0; b < A_BOXES; ++b) tc::prefetch_map(&maps.a[b]);
@@ -556,7 +560,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int quad = warp & 3, half = (warp - FIRST_EPI_WARP) >> 2;
     const int r_in_tile = quad * 32 + lane;
     uint8_t* stage = staging + (warp - FIRST_EPI_WARP) * 2048;
-    uint32_t acc = 0, acc_phase = 0, par = 0, sphase = 0;
+    uint32_t acc = 0, acc_phase = 0, mphase = 0, sphase = 0;
     int slot = 0;
     bool ok = true, ready = false, sready = false;
     for (int tile = first; tile < total; tile += step) {
@@ -656,9 +660,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           c[i] = silu_f32(c[i]) * c[64 + i];
           if (col + i < p.N) m = max_nan(m, fabsf(c[i]));
         }
-        float* mx = s_max + par * 2 * BM;
+        // The quadrant's two warps exchange their maxima, in two buffers in turn: a
+        // warp comes back to a buffer only after its partner has arrived for the
+        // other one, so has read this one. A barrier of their own, with a limit: a
+        // warp may finish up to two tiles of one K block that its partner gave up.
+        float* mx = s_max + mphase * 2 * BM;
         mx[half * BM + r_in_tile] = m;
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(maxima_bar(quad));
+        ok = wait_inline(maxima_bar(quad), mphase, abort_flag, tmo);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        mphase ^= 1u;
         m = max_nan(m, mx[(half ^ 1) * BM + r_in_tile]);
         // rows behind the end hold anything: a scale of 1 keeps their lanes off the
         // division path, which the whole warp would walk with them (64 rows over 8
@@ -676,11 +689,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                        static_cast<uint8_t*>(p.out) + ((int64_t)t.row0 + quad * 32) * p.out_ld + col,
                        p.out_ld, min(32, t.valid - quad * 32), min(64, p.N - col), 4, true);
       }
-      par ^= 1u;
     }
-    // a warp that gave up must not leave its partner waiting for its maxima
-    if (MODE == SWIGLU && !SPLIT && !ok)
-      asm volatile("bar.arrive %0, 64;" ::"r"(1 + quad) : "memory");
   }
 
   if (SPLIT) {

@@ -410,6 +410,38 @@ def test_timeout_is_reported_and_the_context_stays_usable():
     assert moe_get_device_status() == 0
 
 
+# One K block a tile and many tiles a CTA, some of which reach into the second
+# 32 rows and some not: the epilogue's warps exchange row maxima tile by tile.
+ONE_BLOCK_LENS = [3, 40, 1, 128, 20, 70, 33, 0, 5, 256, 31, 64]
+
+
+@pytest.mark.parametrize("K", [16, 128])
+def test_swiglu_of_one_block(K):
+    lens, N = ONE_BLOCK_LENS * 2, 4096
+    E, M = len(lens), sum(lens)
+    offsets = [0]
+    for n in lens:
+        offsets.append(offsets[-1] + n)
+    a, sa, g, sg = operands(M, N, K, E, seed=90)
+    _, _, u, su = operands(1, N, K, E, seed=91)
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    want = swiglu_fp8_block(a, sa, g, u, sg, su, offsets=off)
+    check_swiglu(*want, *swiglu_reference(a, sa, g, sg, u, su, offsets))
+    for _ in range(20):
+        got = swiglu_fp8_block(a, sa, g, u, sg, su, offsets=off)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert moe_get_device_status() == 0
+    # every limit ends in a status, wherever the roles are when it runs out
+    for limit in (1, 100, 1000, 3000, 10000):
+        for _ in range(4):
+            swiglu_fp8_block(a, sa, g, u, sg, su, offsets=off, wait_timeout_ns=limit)
+        torch.cuda.synchronize()
+        assert moe_get_device_status() in (0, _lib.MOE_ERR_DEVICE_TIMEOUT)
+    got = swiglu_fp8_block(a, sa, g, u, sg, su, offsets=off)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert moe_get_device_status() == 0
+
+
 def test_refusals():
     a, sa, w, sw = operands(20, 256, 256, 2, seed=80)
     off = torch.tensor([0, 10, 20], dtype=torch.int32, device="cuda")
