@@ -457,7 +457,7 @@ MOE_API moe_status moe_forward_no_alloc(const moe_dims* dims,
  * p = 0; NaN gives NaN (as does +inf under the softmax).
  * Sums are fp32 over at most 1/148 of the batch, fp64 beyond, in a fixed order:
  * the same inputs give the same bits. Limits: 1 <= k <= 32, k <= E <= 1024,
- * T k < 2^31, num_seqs E < 2^31.
+ * T <= 2^30, T k < 2^31, num_seqs E < 2^31.
  */
 typedef struct {
   int64_t T;                 /* tokens (0 allowed) */
@@ -527,7 +527,8 @@ MOE_API moe_status moe_dequantize_fp8_block(const uint8_t* codes, const float* s
  * any expert may have no rows, and rows before offsets[0] or behind offsets[E]
  * are left as they were. Offsets are read on the device, without a host
  * synchronisation; they must not decrease (values outside 0..M are read as 0 or
- * M). Serving only: there is no gradient.
+ * M; with runs that overlap, what is written is not defined, but stays inside the
+ * M rows). At most 2^30 tiles of 128 x 256 outputs. Serving only: there is no gradient.
  */
 typedef struct {
   int64_t M;                /* rows of A (0 allowed: nothing is written) */

@@ -103,6 +103,7 @@ struct Params {
   int64_t cap;
   int E, M, N;
   int n_tiles, k_blocks, n_blocks;  // tiles along N, blocks of 128 along K and N
+  int max_tiles;                    // that segments without overlaps can have
   const float* a_scale;             // [M][k_blocks]
   const float* w_scale0;            // [E][n_blocks][k_blocks]
   const float* w_scale1;
@@ -419,8 +420,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int u = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += u;
       }
-      if (e < p.E) s_mt[e] = run + incl - v;
-      run += __shfl_sync(0xffffffffu, incl, 31);
+      // Offsets that overlap (an expert has at most 2^24 tiles) must not overflow.
+      constexpr int LIMIT = 1 << 30;
+      if (e < p.E) s_mt[e] = min(LIMIT, run + incl - v);
+      run = min(LIMIT, run + __shfl_sync(0xffffffffu, incl, 31));
     }
     if (lane == 0) s_mt[p.E] = run;
   }
@@ -428,7 +431,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int total = p.n_tiles * s_mt[p.E];  // the host bounds it below 2^31
+  // at most 2^30 by the host; what overlapping offsets ask for beyond is left out
+  const int total = (int)min((long long)p.n_tiles * s_mt[p.E], (long long)p.max_tiles);
   const unsigned long long tmo = p.timeout_ns, drain_tmo = p.drain_timeout_ns;
   // SPLIT: one tile a cluster, this CTA's range of K blocks
   const int first = blockIdx.x / ranks, step = SPLIT ? total : (int)gridDim.x;

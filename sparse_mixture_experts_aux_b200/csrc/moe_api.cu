@@ -648,15 +648,14 @@ moe_status launch_f8b(moe::f8b::Params& p, int64_t rows, int K, const void* a, i
   p.n_blocks = (p.N + BLK - 1) / BLK;
   p.n_tiles = MODE == SWIGLU ? p.n_blocks : (p.n_blocks + 1) / 2;
   // the kernels count tiles in 32 bits
-  if ((static_cast<int64_t>(p.M) / BM + p.E + 1) * p.n_tiles >= (int64_t(1) << 31))
-    return MOE_ERR_UNSUPPORTED;
+  const int64_t max_tiles = (static_cast<int64_t>(p.M) / BM + p.E + 1) * p.n_tiles;
+  if (max_tiles > (int64_t(1) << 30)) return MOE_ERR_UNSUPPORTED;
+  p.max_tiles = static_cast<int>(max_tiles);
   Maps maps;
   memset(&maps, 0, sizeof(maps));
   const uint32_t boxes[A_BOXES] = {16, 64, 128};
   for (int i = 0; i < A_BOXES; ++i)
     if (!encode_map_codes(&maps.a[i], a, K, p.M, 1, lda, boxes[i])) return MOE_ERR_CUDA;
-  if (!encode_map_codes(&maps.w0, w0, K, p.N, p.E, K, BLK)) return MOE_ERR_CUDA;
-  if (MODE == SWIGLU && !encode_map_codes(&maps.w1, w1, K, p.N, p.E, K, BLK)) return MOE_ERR_CUDA;
   if (!encode_map_codes(&maps.w0, w0, K, p.N, p.E, K, BLK) ||
       (MODE == SWIGLU && !encode_map_codes(&maps.w1, w1, K, p.N, p.E, K, BLK)))
     return MOE_ERR_CUDA;
@@ -1173,7 +1172,7 @@ moe_status check_balance(const moe_balance_dims* d) {
       (d->cu_seqlens == nullptr && d->num_seqs != 1) ||
       (d->cu_seqlens != nullptr && !aligned(d->cu_seqlens, 4)))
     return MOE_ERR_INVALID_ARG;
-  if (d->E > moe::tc::MAX_E || d->k > 32 || d->T >= (int64_t(1) << 31) ||
+  if (d->E > moe::tc::MAX_E || d->k > 32 || d->T > (int64_t(1) << 30) ||
       d->T * d->k >= (int64_t(1) << 31) ||
       static_cast<int64_t>(d->num_seqs) * d->E >= (int64_t(1) << 31))
     return MOE_ERR_UNSUPPORTED;

@@ -224,6 +224,20 @@ def test_careless_offsets_stay_inside_the_rows():
                        matmul_fp8_block(a, sa, w, sw, offsets=good))
 
 
+@pytest.mark.parametrize("M", [30, 1000])
+def test_overlapping_offsets_write_nowhere_else(M):
+    E, N, K = 40, 272, 256
+    a, sa, w, sw = operands(M, N, K, E, seed=8)
+    off = torch.tensor([0, M] * (E // 2) + [0], dtype=torch.int32, device="cuda")
+    store = torch.full((M + 256, N + 8), 9.0, dtype=torch.bfloat16, device="cuda")
+    matmul_fp8_block(a, sa, w, sw, offsets=off, out=store[128:128 + M, :N])
+    assert (store[:128] == 9.0).all() and (store[128 + M:] == 9.0).all() and (store[:, N:] == 9.0).all()
+    off = torch.tensor([0] * E + [M], dtype=torch.int32, device="cuda")   # the last expert has them all
+    want = matmul_fp8_block(a, sa, w[-1], sw[-1])
+    assert torch.equal(matmul_fp8_block(a, sa, w, sw, offsets=off), want)
+    assert moe_get_device_status() == 0
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 200, 384), (300, 264, 640)])
 def test_strides_and_float8_views(M, N, K):
     a, sa, w, sw = operands(M, N, K, 0, seed=7)

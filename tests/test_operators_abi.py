@@ -52,6 +52,15 @@ def test_balance_pointers():
     assert _lib.moe_balance_loss_backward(balance(T=0), 0, 0, 0, 0, 0) == _lib.MOE_OK
 
 
+def test_balance_token_limit():
+    # the kernels count tokens, a block's look-ahead included, in 32 bits
+    assert _lib.moe_balance_loss_workspace_size(balance(T=1 << 30, k=1)) > 0
+    for T in ((1 << 30) + 1, (1 << 31) - 1):
+        assert _lib.moe_balance_loss_workspace_size(balance(T=T, k=1)) == 0
+        assert _lib.moe_balance_loss(balance(T=T, k=1), P, P, P, P, P) == UNSUPPORTED
+        assert _lib.moe_balance_loss_backward(balance(T=T, k=1), P, P, P, P, P) == UNSUPPORTED
+
+
 def test_balance_workspace_covers_every_chunk_and_sequence():
     for T, S, E in [(1, 1, 8), (148 * 32, 1, 8), (148 * 32 + 1, 5, 256), (1 << 20, 4096, 64)]:
         chunk = max(32, -(-T // 148))
