@@ -14,9 +14,8 @@
 //
 // Bound: memory in principle (15 us for 32768 rows of 256 experts, both ways),
 // in fact the instructions of a row and the three launches: 37 us. The forward
-// pass reads the logits once, the gradient reads
-// them once more and writes as much (it needs f, a count over the whole
-// sequence). A row's softmax stays in the registers of one group of lanes.
+// pass reads the logits once, the gradient reads them once more and writes as
+// much (it needs f, a count over the whole sequence). A row's softmax stays in the registers of one group of lanes.
 // Determinism: every sum has a fixed order (lane, then warp, then chunk);
 // counts are integers. The probability sums of a warp are fp32 over at most
 // one chunk of a sequence; everything above is fp64.
@@ -179,8 +178,8 @@ __device__ __forceinline__ float loss_of(double dot, int n, int E, int k) {
 }
 
 // One block per chunk of tokens; warps take the chunk's tokens in turn, 32 / G
-// times ROWS_AT_ONCE at a time. The block walks the sequences that its chunk meets; each leaves
-// its sums in slot (chunk + sequence), which no other pair has, or, when the
+// times ROWS_AT_ONCE at a time. The block walks the sequences that its chunk
+// meets; each leaves its sums in slot (chunk + sequence), which no other pair has, or, when the
 // sequence lies inside the chunk, its results at once.
 // Dynamic shared memory: float psum[warps][E], int32 counts[E].
 template <typename TL, int G, int NV, bool SIG>

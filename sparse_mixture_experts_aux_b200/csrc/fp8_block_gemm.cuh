@@ -39,8 +39,7 @@
 // over 64 rows 160 us in the layer, 5.9 TB/s, 0.90 of the measured copy. Not
 // kept, as slower: CTA pairs (tcgen05 cta_group::2; 171 us where this form takes
 // 150), four TMEM buffers of 128 columns (173), loading a block's first columns
-// while the last block is added (169), a ring of five or six stages for few rows
-// (182 -> 189).
+// while the last block is added (169), a deeper ring for few rows (181 -> 189 us).
 //
 // Tiles of 128 rows never straddle two experts; rows of a tile behind its
 // expert's last row are computed from whatever lies there and not stored (a
