@@ -392,6 +392,23 @@ def test_repeat_streams_and_graph_give_the_same_bits():
         assert torch.equal(c, w)
 
 
+def test_two_streams_at_once():
+    # a persistent launch beside clusters that share a tile, each on its own stream
+    a, sa, w, sw = operands(1500, 1024, 2048, 0, seed=60)
+    big = matmul_fp8_block(a, sa, w, sw)
+    small = swiglu_fp8_block(a[:3], sa[:3], w, w, sw, sw)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        got.append((matmul_fp8_block(a, sa, w, sw, stream=s1),
+                    swiglu_fp8_block(a[:3], sa[:3], w, w, sw, sw, stream=s2)))
+    torch.cuda.synchronize()
+    for x, y in got:
+        assert torch.equal(x, big) and torch.equal(y[0], small[0]) and torch.equal(y[1], small[1])
+    assert moe_get_device_status() == 0
+
+
 def test_no_rows():
     a, sa, w, sw = operands(4, 256, 256, 0)
     assert matmul_fp8_block(a[:0], sa[:0], w, sw).shape == (0, 256)

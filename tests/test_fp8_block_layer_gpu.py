@@ -2,6 +2,8 @@
 against fp64 on what the stage before left in the workspace: the routed rows'
 codes bit by bit, H within the bounds of test_fp8_block_gpu.py, and y within the
 roundings of its own stage; then the routing and the balance loss behind it."""
+import ctypes
+
 import pytest
 import torch
 
@@ -124,6 +126,27 @@ def test_repeat_graph_and_no_alloc_give_the_same_bits():
                               w.k, 0.0, y, aux, counts)
     torch.cuda.synchronize()
     assert torch.equal(y, want[0])
+
+
+@pytest.mark.parametrize("w", [CASES[1], CASES[4], CASES[5]], ids=lambda w: w.name)
+def test_debug_build_is_silent_and_bit_identical(w):
+    inp = make_inputs(w, device="cuda")
+    q = quantised(inp)
+    ws = Workspace()
+    want = run(w, inp, q, ws)
+    dbg, p = _lib.load_debug(), _lib._ptr
+    buf = torch.empty_like(ws.buf)
+    dims = make_dims(w.T, w.d, w.d_e, 0, _lib.MOE_BF16, inp["router_bias"], buf, buf.numel(),
+                     torch.cuda.current_stream().cuda_stream,
+                     weight_format=_lib.MOE_WEIGHTS_FP8_BLOCK, weight_scales=q["scales"])
+    got = [torch.empty_like(t) for t in want]
+    st = dbg.moe_forward(ctypes.byref(dims), p(inp["x"]), p(inp["W_r"]), p(q["W_g"]), p(q["W_u"]),
+                         p(q["W_d"]), None, w.E, w.k, w.capacity_factor, *map(p, got))
+    assert st == _lib.MOE_OK
+    torch.cuda.synchronize()
+    assert dbg.moe_get_device_status() == _lib.MOE_OK
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
 
 
 def test_empty_batch():
