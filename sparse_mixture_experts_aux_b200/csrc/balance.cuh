@@ -82,12 +82,15 @@ __device__ __forceinline__ float rcp(float x) {
 // The terms of one row's probabilities in place of its logits; returns the
 // factor that makes them probabilities. SIGMOID: also the slope 1 - sigmoid(r).
 // Lane l of a group of G holds experts l, l + G, ... (NV of them; those past E
-// hold -inf). A softmax is scaled by the row's largest logit: 2^(r log2e - c), c
-// = max log2e rounded once, an error that all terms share and the factor takes
-// out. sigmoid(r) = e^min(r,0) / (1 + e^-|r|) needs one exponential where the
-// row has a logit >= 0; a row below zero is scaled by its largest logit too, so
-// that it keeps its ratios where the sigmoids underflow. A row of only -inf has
-// no probabilities: all zero. NaN gives NaN, as does +inf under the softmax.
+// hold -inf). A softmax is scaled by the row's largest logit: 2^((r - max)
+// log2e). The difference is taken first, in logits: it is exact near the maximum
+// and finite or -inf for any finite row. As one fused r log2e - max log2e, the
+// rounding of max log2e passes the exponent's range from logits of 1e9 on (rows
+// of 1e10 had no probabilities, or NaN). sigmoid(r) = e^min(r,0) / (1 + e^-|r|)
+// needs one exponential where the row has a logit >= 0; a row below zero is
+// scaled by its largest logit too, so that it keeps its ratios where the
+// sigmoids underflow. A row of only -inf has no probabilities: all zero. NaN
+// gives NaN, as does +inf under the softmax.
 // U rows at once, so that their shuffles overlap.
 template <int G, int NV, int U, bool SIG>
 __device__ __forceinline__ void row_terms(float (*v)[NV], float (*slope)[NV], float* inv) {
@@ -108,22 +111,22 @@ __device__ __forceinline__ void row_terms(float (*v)[NV], float (*slope)[NV], fl
     s[u] = 0.f;
     if (SIG) {
       const bool below = __any_sync(0xffffffffu, m[u] < 0.f);  // warp-uniform
-      const float c = (m[u] < 0.f && m[u] != -INFINITY ? m[u] : 0.f) * -L2E;
+      const float top_r = m[u] < 0.f && m[u] != -INFINITY ? m[u] : 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const float e = ex2(fabsf(v[u][i]) * -L2E), r1 = rcp(1.f + e);
         const bool pos = v[u][i] >= 0.f;
         float top = pos ? 1.f : e;
-        if (below && !pos) top = ex2(fmaf(v[u][i], L2E, c));
+        if (below && !pos) top = ex2((v[u][i] - top_r) * L2E);
         slope[u][i] = (pos ? e : 1.f) * r1;
         v[u][i] = top * r1;
         s[u] += v[u][i];
       }
     } else {
-      const float c = (m[u] != -INFINITY ? m[u] : 0.f) * -L2E;
+      const float top_r = m[u] != -INFINITY ? m[u] : 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        v[u][i] = ex2(fmaf(v[u][i], L2E, c));
+        v[u][i] = ex2((v[u][i] - top_r) * L2E);
         s[u] += v[u][i];
       }
     }

@@ -414,3 +414,20 @@ def test_long_batch_sums_stay_exact():
     assert counts[0, 0].item() == T and tokens.item() == T
     assert abs(loss.item() - want) <= (eps_p(E, 6.0) + 43 * 2.0 ** -24) * want
     assert np.isfinite(loss.item())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("gate_mode", [0, 1, 2])
+@pytest.mark.parametrize("E", [7, 12, 40, 300])
+def test_rows_far_from_zero(E, gate_mode, dtype):
+    # finite rows whose largest logit is far from zero, up to the type's last value:
+    # r - max rounds by half an ulp of itself whatever max is, so eps_p holds with R
+    # the differences that still count (e^-100 of the largest term is zero in fp32)
+    top = torch.finfo(dtype).max
+    far = [s * v for v in (1e4, 1e9, 1e10, 1e12, 1e30, top) for s in (1.0, -1.0)]
+    logits, idx = draw(4 * len(far), E, 2, dtype, seed=17)
+    for i, v in enumerate(far):
+        logits[4 * i] = v                         # equal logits: as likely as one another
+        logits[4 * i + 1] = (logits[4 * i + 1].float() + v).clamp(-top, top).to(dtype)
+        logits[4 * i + 2, 3] = v                  # one among ordinary ones
+    check(logits, idx, gate_mode, spread=100.0)
