@@ -2,37 +2,13 @@
 argument checks and marshalling; the library computes."""
 from __future__ import annotations
 
-import contextlib
 from typing import Optional
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _lib
+from . import _lib, streams
 from .layer import Workspace, dtype_code
-
-
-def _handle(stream, dev) -> int:
-    """cudaStream_t to enqueue on: the device's current stream unless one is given."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-
-
-def _on(dev):
-    """A context with `dev` current (the library launches on the current device)."""
-    return _HERE if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
-
-
-_HERE = contextlib.nullcontext()
-
-
-def _lend(t: torch.Tensor, stream) -> None:
-    """Tell torch's allocator that `t`, allocated on the current stream, is used on `stream`."""
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=t.device)
-        t.record_stream(stream)
 
 
 def _need(name: str, t: torch.Tensor, dtype, shape, dev) -> None:
@@ -82,21 +58,22 @@ def _forward(logits, topk_idx, gate_mode, token_mask, cu_seqlens, workspace, str
     T, E, S, fields = _args(logits, k, gate_mode, token_mask, cu_seqlens)
     dev = logits.device
     _need("topk_idx", topk_idx, torch.int32, (T, k), dev)
-    with _on(dev):
-        d = _lib.moe_balance_dims(*fields, None, 0, _handle(stream, dev))
+    handle, side = streams.run_on(stream, dev)
+    with streams.on(dev, side):
+        d = _lib.moe_balance_dims(*fields, None, 0, handle)
         need = _lib.moe_balance_loss_workspace_size(d) if T > _lib.MOE_BALANCE_SMALL_T else 0
         if need:  # a call that is refused has no size: it says why below
             ws = (workspace or Workspace()).get(need, dev)
             d.workspace, d.workspace_bytes = ws.data_ptr(), ws.numel()
-            _lend(ws, stream)
+            streams.lend(side, ws)
         loss = torch.empty(S, dtype=torch.float32, device=dev)
         counts = torch.empty((S, E), dtype=torch.int32, device=dev)
         tokens = torch.empty(S, dtype=torch.int32, device=dev)
-        for t in (loss, counts, tokens):
-            _lend(t, stream)
         rc = _lib.moe_balance_loss(d, logits, topk_idx, loss, counts, tokens)
     if rc != _lib.MOE_OK:
         raise _lib.MoeError(rc, "moe_balance_loss")
+    streams.lend(side, logits, topk_idx, token_mask, cu_seqlens)
+    streams.give(side, dev, loss, counts, tokens)
     return loss, counts, tokens
 
 
@@ -116,13 +93,15 @@ def balance_loss_backward(dloss: torch.Tensor, logits: torch.Tensor, counts: tor
     _need("dloss", dloss, torch.float32, (S,), dev)
     _need("counts", counts, torch.int32, (S, E), dev)
     _need("tokens", tokens, torch.int32, (S,), dev)
-    with _on(dev):
-        d = _lib.moe_balance_dims(*fields, None, 0, _handle(stream, dev))
+    handle, side = streams.run_on(stream, dev)
+    with streams.on(dev, side):
+        d = _lib.moe_balance_dims(*fields, None, 0, handle)
         dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
-        _lend(dlogits, stream)
         rc = _lib.moe_balance_loss_backward(d, dloss, logits, counts, tokens, dlogits)
     if rc != _lib.MOE_OK:
         raise _lib.MoeError(rc, "moe_balance_loss_backward")
+    streams.lend(side, dloss, logits, counts, tokens, token_mask, cu_seqlens)
+    streams.give(side, dev, dlogits)
     return dlogits
 
 
@@ -165,7 +144,9 @@ def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, gate_mode: int = 
     gate_mode: as in forward (2: the probabilities are normalised sigmoids).
     token_mask bool or uint8 [T]: False for padding tokens.
     cu_seqlens int32 [S + 1]: sequence s is tokens cu[s] .. cu[s + 1] - 1.
-    stream: where to run, as in forward (not with a gradient: use torch.cuda.stream).
+    stream: where to run instead of the current stream (not with a gradient: use
+    torch.cuda.stream). The inputs must be ready there, and the results are: wait
+    for it before they are used elsewhere. Both may be dropped at any time.
     """
     if torch.is_grad_enabled() and logits.requires_grad:
         if stream is not None:

@@ -1,13 +1,17 @@
 """Torch-facing wrappers of the block-scaled FP8 operators (include/moe.h,
-moe_*_fp8_block): argument checks and marshalling; the library computes."""
+moe_*_fp8_block): argument checks and marshalling; the library computes.
+
+stream= in each of them: where to run instead of the current stream. The inputs
+must be ready there, and the results are: wait for it before they are used
+elsewhere. Both may be dropped at any time."""
 from __future__ import annotations
 
 from typing import Optional
 
 import torch
 
-from . import _lib
-from .balance import _handle, _lend, _need, _on
+from . import _lib, streams
+from .balance import _need
 from .layer import dtype_code
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)
@@ -38,19 +42,20 @@ def quantize_fp8_block(w: torch.Tensor, block_rows: int = 128, stream=None):
     for n in w.shape[:-2]:
         stack *= n
     dev = w.device
-    with _on(dev):
+    handle, side = streams.run_on(stream, dev)
+    with streams.on(dev, side):
         codes = torch.empty(w.shape, dtype=torch.uint8, device=dev)
         srows = rows if block_rows == 1 else _ceil(rows, max(1, block_rows))
         scales = torch.empty((*w.shape[:-2], srows, _ceil(cols, 128)), dtype=torch.float32,
                              device=dev)
-        for t in (codes, scales):
-            _lend(t, stream)
         if w.numel() == 0 and cols > 0:
             return codes, scales
         rc = _lib.moe_quantize_fp8_block(w, dtype_code(w.dtype), stack, rows, cols, ld, block_rows,
-                                         codes, scales, _handle(stream, dev))
+                                         codes, scales, handle)
     if rc != _lib.MOE_OK:
         raise _lib.MoeError(rc, "moe_quantize_fp8_block")
+    streams.lend(side, w)
+    streams.give(side, dev, codes, scales)
     return codes, scales
 
 
@@ -63,15 +68,17 @@ def dequantize_fp8_block(codes: torch.Tensor, scales: torch.Tensor, block_rows: 
     dev = codes.device
     srows = rows if block_rows == 1 else _ceil(rows, max(1, block_rows))
     _need("scales", scales, torch.float32, codes.shape[:-2] + (srows, _ceil(cols, 128)), dev)
-    with _on(dev):
+    handle, side = streams.run_on(stream, dev)
+    with streams.on(dev, side):
         out = torch.empty(codes.shape, dtype=torch.float32, device=dev)
-        _lend(out, stream)
         if codes.numel() == 0 and cols > 0:
             return out
         rc = _lib.moe_dequantize_fp8_block(codes, scales, codes.numel() // (rows * cols), rows, cols,
-                                           block_rows, out, _handle(stream, dev))
+                                           block_rows, out, handle)
     if rc != _lib.MOE_OK:
         raise _lib.MoeError(rc, "moe_dequantize_fp8_block")
+    streams.lend(side, codes, scales)
+    streams.give(side, dev, out)
     return out
 
 
@@ -126,20 +133,23 @@ def matmul_fp8_block(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor,
     if row_scale is not None:
         _need("row_scale", row_scale, torch.float32, (M,), dev)
         d.row_scale = row_scale.data_ptr()
-    with _on(dev):
+    handle, side = streams.run_on(stream, dev)
+    with streams.on(dev, side):
         if out is None:
             out = torch.empty(M, N, dtype=out_dtype, device=dev)
-            _lend(out, stream)
         elif out.device != dev or tuple(out.shape) != (M, N):
             raise RuntimeError(f"out must be [{M}, {N}] on {dev}")
         elif (N > 1 and out.stride(1) != 1) or (M > 1 and out.stride(0) < N):
             raise RuntimeError("out must have its columns next to each other (rows may be strided)")
         d.out_dtype = dtype_code(out.dtype)
         d.ld_out = out.stride(0) if M > 1 else N
-        d.stream = _handle(stream, dev) or None
+        d.stream = handle or None
         rc = _lib.moe_matmul_fp8_block(d, a, a_scales, w, w_scales, out)
     if rc != _lib.MOE_OK:
         raise _lib.MoeError(rc, "moe_matmul_fp8_block")
+    if side is not None:  # out may be the caller's or the call's own
+        streams.lend(side, a, a_scales, w, w_scales, offsets, row_scale, out)
+        streams.give(side, dev, out)
     return out
 
 
@@ -157,19 +167,21 @@ def swiglu_fp8_block(a: torch.Tensor, a_scales: torch.Tensor, W_g: torch.Tensor,
     """
     d, M, N = _product_dims(a, a_scales, (W_g, W_u), (g_scales, u_scales), offsets, wait_timeout_ns)
     dev = a.device
-    with _on(dev):
+    handle, side = streams.run_on(stream, dev)
+    with streams.on(dev, side):
         if codes is None:
             codes = torch.empty(M, N, dtype=torch.uint8, device=dev)
-            _lend(codes, stream)
         else:
             _need("codes", codes, _CODES, (M, N), dev)
         if scales is None:
             scales = torch.empty(M, _ceil(N, 128), dtype=torch.float32, device=dev)
-            _lend(scales, stream)
         else:
             _need("scales", scales, torch.float32, (M, _ceil(N, 128)), dev)
-        d.stream = _handle(stream, dev) or None
+        d.stream = handle or None
         rc = _lib.moe_swiglu_fp8_block(d, a, a_scales, W_g, W_u, g_scales, u_scales, codes, scales)
     if rc != _lib.MOE_OK:
         raise _lib.MoeError(rc, "moe_swiglu_fp8_block")
+    if side is not None:  # codes and scales may be the caller's or the call's own
+        streams.lend(side, a, a_scales, W_g, W_u, g_scales, u_scales, offsets, codes, scales)
+        streams.give(side, dev, codes, scales)
     return codes, scales
