@@ -6,7 +6,7 @@ from typing import Optional
 
 import torch
 
-from . import _lib
+from . import _lib, streams
 
 
 def dtype_code(dt: torch.dtype) -> int:
@@ -79,6 +79,9 @@ def forward(x: torch.Tensor, W_r: torch.Tensor, W_g: torch.Tensor, W_u: torch.Te
     as uint8 E4M3 codes and weight_scales = their 128 x 128 block scales
     (quantize_fp8_block), concatenated [W_g | W_u | W_d]; E4M3 activations with a
     scale for each 128 columns inside the experts.
+    stream: where to run instead of the current stream. The inputs must be ready
+    there, and the results are: wait for it before they are used elsewhere. Both may
+    be dropped at any time.
     wait_timeout_ns: limit of the GEMM kernels' device-side waits (0 = library default).
     gate_mode / selection_bias / n_group / topk_group: routing variants (include/moe.h).
     """
@@ -89,10 +92,7 @@ def forward(x: torch.Tensor, W_r: torch.Tensor, W_g: torch.Tensor, W_u: torch.Te
             raise RuntimeError(f"{name} must be contiguous")
     E = W_r.shape[0]
     dev = x.device
-    if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
-    elif isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
+    stream, side = streams.run_on(stream, dev)
     workspace = workspace or Workspace()
     routing = dict(gate_mode=gate_mode, selection_bias=selection_bias, n_group=n_group,
                    topk_group=topk_group)
@@ -115,13 +115,18 @@ def forward(x: torch.Tensor, W_r: torch.Tensor, W_g: torch.Tensor, W_u: torch.Te
     nbytes = _lib.moe_workspace_size(probe, E, k, capacity_factor)
     if nbytes == 0:
         raise _lib.MoeError(_lib.MOE_ERR_INVALID_ARG, "moe_workspace_size")
-    ws = workspace.get(nbytes, dev)
-    dims = _dims_for(x, W_g, d_s, router_bias, ws, stream, events, wait_timeout_ns, routing,
-                     weight_scales, act_fp8, weight_block_scales, fp8_block)
-    y = torch.empty_like(x) if y is None else y
-    aux = torch.empty(1, dtype=torch.float32, device=dev) if aux is None else aux
-    counts = torch.empty(E, dtype=torch.int32, device=dev) if counts is None else counts
-    _lib.moe_forward(dims, x, W_r, W_g, W_u, W_d, W_shared, E, k, capacity_factor, y, aux, counts)
+    with streams.on(dev, side):
+        ws = workspace.get(nbytes, dev)
+        dims = _dims_for(x, W_g, d_s, router_bias, ws, stream, events, wait_timeout_ns, routing,
+                         weight_scales, act_fp8, weight_block_scales, fp8_block)
+        y = torch.empty_like(x) if y is None else y
+        aux = torch.empty(1, dtype=torch.float32, device=dev) if aux is None else aux
+        counts = torch.empty(E, dtype=torch.int32, device=dev) if counts is None else counts
+        _lib.moe_forward(dims, x, W_r, W_g, W_u, W_d, W_shared, E, k, capacity_factor, y, aux, counts)
+    if side is not None:  # y, aux and counts may be the caller's or the call's own
+        streams.lend(side, ws, x, W_r, W_g, W_u, W_d, W_shared, router_bias, selection_bias,
+                     weight_scales, weight_block_scales, y, aux, counts)
+        streams.give(side, dev, y, aux, counts)
     return y, aux, counts
 
 
@@ -132,12 +137,15 @@ def quantize_fp8(w: torch.Tensor, stream=None):
         raise RuntimeError("w must be a contiguous CUDA tensor")
     cols = w.shape[-1]
     rows = w.numel() // cols
-    codes = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
-    scales = torch.empty(w.shape[:-1], dtype=torch.float32, device=w.device)
-    st = torch.cuda.current_stream(w.device).cuda_stream if stream is None else stream
-    rc = _lib.moe_quantize_fp8(w, dtype_code(w.dtype), rows, cols, codes, scales, st)
+    st, side = streams.run_on(stream, w.device)
+    with streams.on(w.device, side):
+        codes = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
+        scales = torch.empty(w.shape[:-1], dtype=torch.float32, device=w.device)
+        rc = _lib.moe_quantize_fp8(w, dtype_code(w.dtype), rows, cols, codes, scales, st)
     if rc != _lib.MOE_OK:
         raise _lib.MoeError(rc, "moe_quantize_fp8")
+    streams.lend(side, w)
+    streams.give(side, w.device, codes, scales)
     return codes, scales
 
 
@@ -145,11 +153,14 @@ def dequantize_fp8(codes: torch.Tensor, scales: torch.Tensor, stream=None) -> to
     """fp32 weights code * scale, as the FP8 layer computes with them (moe_dequantize_fp8)."""
     cols = codes.shape[-1]
     rows = codes.numel() // cols
-    out = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
-    st = torch.cuda.current_stream(codes.device).cuda_stream if stream is None else stream
-    rc = _lib.moe_dequantize_fp8(codes, scales, rows, cols, out, st)
+    st, side = streams.run_on(stream, codes.device)
+    with streams.on(codes.device, side):
+        out = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
+        rc = _lib.moe_dequantize_fp8(codes, scales, rows, cols, out, st)
     if rc != _lib.MOE_OK:
         raise _lib.MoeError(rc, "moe_dequantize_fp8")
+    streams.lend(side, codes, scales)
+    streams.give(side, codes.device, out)
     return out
 
 
@@ -162,13 +173,16 @@ def quantize_mxfp4(w: torch.Tensor, stream=None):
         raise RuntimeError("w must be a contiguous CUDA tensor")
     cols = w.shape[-1]
     rows = w.numel() // cols
-    codes = torch.empty(*w.shape[:-1], cols // 2, dtype=torch.uint8, device=w.device)
-    bscales = torch.empty(*w.shape[:-1], cols // 32, dtype=torch.uint8, device=w.device)
-    factors = torch.empty(w.shape[:-1], dtype=torch.float32, device=w.device)
-    st = torch.cuda.current_stream(w.device).cuda_stream if stream is None else stream
-    rc = _lib.moe_quantize_mxfp4(w, dtype_code(w.dtype), rows, cols, codes, bscales, factors, st)
+    st, side = streams.run_on(stream, w.device)
+    with streams.on(w.device, side):
+        codes = torch.empty(*w.shape[:-1], cols // 2, dtype=torch.uint8, device=w.device)
+        bscales = torch.empty(*w.shape[:-1], cols // 32, dtype=torch.uint8, device=w.device)
+        factors = torch.empty(w.shape[:-1], dtype=torch.float32, device=w.device)
+        rc = _lib.moe_quantize_mxfp4(w, dtype_code(w.dtype), rows, cols, codes, bscales, factors, st)
     if rc != _lib.MOE_OK:
         raise _lib.MoeError(rc, "moe_quantize_mxfp4")
+    streams.lend(side, w)
+    streams.give(side, w.device, codes, bscales, factors)
     return codes, bscales, factors
 
 
@@ -177,11 +191,14 @@ def dequantize_mxfp4(codes: torch.Tensor, bscales: torch.Tensor, factors: torch.
     """fp32 weights code * 2^X, as the MXFP4 layer computes with them (moe_dequantize_mxfp4)."""
     cols = codes.shape[-1] * 2
     rows = codes.numel() * 2 // cols
-    out = torch.empty(*codes.shape[:-1], cols, dtype=torch.float32, device=codes.device)
-    st = torch.cuda.current_stream(codes.device).cuda_stream if stream is None else stream
-    rc = _lib.moe_dequantize_mxfp4(codes, bscales, factors, rows, cols, out, st)
+    st, side = streams.run_on(stream, codes.device)
+    with streams.on(codes.device, side):
+        out = torch.empty(*codes.shape[:-1], cols, dtype=torch.float32, device=codes.device)
+        rc = _lib.moe_dequantize_mxfp4(codes, bscales, factors, rows, cols, out, st)
     if rc != _lib.MOE_OK:
         raise _lib.MoeError(rc, "moe_dequantize_mxfp4")
+    streams.lend(side, codes, bscales, factors)
+    streams.give(side, codes.device, out)
     return out
 
 

@@ -4,8 +4,11 @@ streams other than the caller's for inputs and results."""
 import pytest
 import torch
 
-from sparse_mixture_experts_aux_b200 import (balance_loss, balance_loss_backward, dequantize_fp8_block,
-                                             matmul_fp8_block, quantize_fp8_block, swiglu_fp8_block)
+from sparse_mixture_experts_aux_b200 import (Workspace, balance_loss, balance_loss_backward,
+                                             dequantize_fp8, dequantize_fp8_block, dequantize_mxfp4,
+                                             forward, matmul_fp8_block, quantize_fp8,
+                                             quantize_fp8_block, quantize_mxfp4, swiglu_fp8_block)
+from sparse_mixture_experts_aux_b200.inputs import Workload, make_inputs
 from tests.test_balance_loss_gpu import draw
 from tests.test_fp8_block_gpu import operands
 
@@ -54,9 +57,7 @@ def same(got, want):
         assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("name", NAMES)
-def test_results_do_not_take_memory_the_current_stream_still_uses(name):
-    inputs, call = calls(31)[name]
+def results_do_not_take_memory(inputs, call):
     want = call(inputs)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -78,11 +79,8 @@ def test_results_do_not_take_memory_the_current_stream_still_uses(name):
         assert (k == 1).all()
 
 
-@pytest.mark.parametrize("name", NAMES)
-def test_inputs_and_results_may_be_dropped(name):
+def inputs_and_results_may_be_dropped(first, second, call):
     side = torch.cuda.Stream()
-    first, call = calls(32)[name]
-    second = calls(33)[name][0]
     want, other = call(first), call(second)
     torch.cuda.synchronize()
     torch.cuda.empty_cache()
@@ -107,6 +105,17 @@ def test_inputs_and_results_may_be_dropped(name):
     assert all((j == 0).all() for j in junk)
 
 
+@pytest.mark.parametrize("name", NAMES)
+def test_results_do_not_take_memory_the_current_stream_still_uses(name):
+    results_do_not_take_memory(*calls(31)[name])
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_inputs_and_results_may_be_dropped(name):
+    first, call = calls(32)[name]
+    inputs_and_results_may_be_dropped(first, calls(33)[name][0], call)
+
+
 def test_raw_handles_and_the_default_stream():
     for name, (inputs, call) in calls(34).items():
         want = call(inputs)
@@ -120,3 +129,71 @@ def test_raw_handles_and_the_default_stream():
         torch.cuda.synchronize()
         for g in got:
             same(g, want)
+
+
+def layer_calls(seed):
+    inp = make_inputs(Workload("streams", 300, 256, 8, 256, 2, seed=seed), device="cuda")
+    names = ("W_g", "W_u", "W_d")
+    plain = [inp["x"], inp["W_r"]] + [inp[n] for n in names]
+    block = [quantize_fp8_block(inp[n], 128) for n in names]
+    scales = torch.cat([s.reshape(-1) for _, s in block])
+    w = inp["W_g"].reshape(-1, 256)
+    c8, s8 = quantize_fp8(w)
+    mx = quantize_mxfp4(w)
+    return {
+        "forward": (plain, lambda t, **kw: forward(*t, k=2, **kw)),
+        "forward fp8 blocks": (plain[:2] + [c for c, _ in block] + [scales],
+                               lambda t, **kw: forward(*t[:5], k=2, weight_scales=t[5], fp8_block=True, **kw)),
+        "quantize fp8": ([w], lambda t, **kw: quantize_fp8(t[0], **kw)),
+        "dequantize fp8": ([c8, s8], lambda t, **kw: (dequantize_fp8(*t, **kw),)),
+        "quantize mxfp4": ([w], lambda t, **kw: quantize_mxfp4(t[0], **kw)),
+        "dequantize mxfp4": (list(mx), lambda t, **kw: (dequantize_mxfp4(*t, **kw),)),
+    }
+
+
+LAYER = ["forward", "forward fp8 blocks", "quantize fp8", "dequantize fp8", "quantize mxfp4",
+         "dequantize mxfp4"]
+
+
+@pytest.mark.parametrize("name", LAYER)
+def test_layer_results_do_not_take_memory_the_current_stream_still_uses(name):
+    results_do_not_take_memory(*layer_calls(35)[name])
+
+
+@pytest.mark.parametrize("name", LAYER)
+def test_layer_inputs_and_results_may_be_dropped(name):
+    first, call = layer_calls(36)[name]
+    inputs_and_results_may_be_dropped(first, layer_calls(37)[name][0], call)
+
+
+@pytest.mark.parametrize("name", LAYER)
+def test_layer_raw_handles(name):
+    inputs, call = layer_calls(38)[name]
+    want = call(inputs)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [call(inputs, stream=s) for s in (side, side.cuda_stream, 0)]
+    torch.cuda.synchronize()
+    for g in got:
+        same(g, want)
+
+
+def test_layer_workspace_lent_to_another_stream():
+    # a workspace of the caller's, made on the current stream, dropped while the
+    # side stream still runs in it
+    inp = make_inputs(Workload("streams", 300, 256, 8, 256, 2, seed=39), device="cuda")
+    args = [inp[n] for n in ("x", "W_r", "W_g", "W_u", "W_d")]
+    want = forward(*args, k=2)
+    ws = Workspace()
+    forward(*args, k=2, workspace=ws)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        busy()
+    got = forward(*args, k=2, workspace=ws, stream=side)
+    size = ws.buf.numel()
+    del ws
+    junk = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    same(got, want)
+    assert not junk.any()
