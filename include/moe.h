@@ -522,7 +522,8 @@ MOE_API moe_status moe_dequantize_fp8_block(const uint8_t* codes, const float* s
  * Products on that format, dense or grouped by expert:
  *   C[m, n] = sum_b sA[m, b] sW[n / 128, b] sum_{k in block b} A[m, k] W[n, k]
  * in fp32, rounded once to the output type. Each K block is summed by the tensor
- * cores, then added, times its scales, to fp32 accumulators.
+ * cores, then added, times its scales, to fp32 accumulators; the scales' own product
+ * may lie outside the normal fp32 numbers, as long as the scaled sums do not.
  * Grouped (E > 0): rows offsets[e] .. offsets[e + 1] - 1 meet expert e's matrix;
  * any expert may have no rows, and rows before offsets[0] or behind offsets[E]
  * are left as they were. Offsets are read on the device, without a host

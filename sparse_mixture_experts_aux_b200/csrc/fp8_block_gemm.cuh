@@ -75,7 +75,8 @@ constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * SCALE_SLOTS + 4;
 static_assert(8 * NUM_BARS + 8 <= BAR_BYTES, "barriers, TMEM address, abort flag");
 struct ScaleSlot {
   float a[GROUP][BM];            // the rows' scales
-  float2 w[GROUP];               // the weight scales of the tile's two halves
+  float4 w[GROUP];               // the weight scales of the tile's two halves; z: some product
+                                 // of a row's scale with one of them is no normal number
   int e, nb, row0, valid;        // the tile, in its first group
 };
 constexpr int MAX_BYTES = 2 * 2 * BM * 4;  // SWIGLU: row maxima of the two half tiles, double-buffered
@@ -153,6 +154,31 @@ __device__ __forceinline__ void pass_regs(uint32_t* r) {
 __device__ __forceinline__ void promote32(float* acc, const uint32_t* r, float m) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) acc[i] = fmaf(m, __uint_as_float(r[i]), acc[i]);
+}
+// The product of two scales as fp32 holds it, and outside the normal numbers that
+// of one scale times 2^64 or of both times 2^-64; the sums then take the rest, 2^-64
+// or 2^128, first. They are exact through it: a nonzero one lies within 2^-18 ..
+// 2^25. So a scaled sum that fp32 can hold comes out as it should, where the plain
+// product would have lost bits to a subnormal, or made inf of a number and NaN of a
+// zero. What still under- or overflows here does so in the scaled sum itself.
+__device__ __forceinline__ bool scales_fit(float a, float w) {
+  const float m = fabsf(a * w);
+  return (m >= FLT_MIN && m <= FLT_MAX) || a == 0.f || w == 0.f;
+}
+__device__ __noinline__ float2 far_scales(float a, float w) {
+  const float m = a * w;
+  if (scales_fit(a, w)) return make_float2(m, 1.f);
+  if (fabsf(m) < FLT_MIN) {  // the smaller of the two is far below one
+    const bool less = fabsf(a) < fabsf(w);
+    return make_float2((less ? a : w) * 0x1p64f * (less ? w : a), 0x1p-64f);
+  }
+  return make_float2(a * 0x1p-64f * (w * 0x1p-64f), 0x1p64f);  // the sums' factor twice
+}
+// r times what far_scales left to the sums.
+__device__ __forceinline__ void scale32(uint32_t* r, float f) {
+  const float g = f > 1.f ? f : 1.f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f * g);
 }
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   float4 v;
@@ -543,11 +569,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ok = wait_ctrl(sempty_bar(slot), phase ^ 1u);
           if (!ok) break;
           ScaleSlot& s = slots[slot];
+          // lane k of the first GROUP keeps whether block k has products far out
+          bool far = false;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int k = 0; k < GROUP; ++k) {
+            const float wa = __shfl_sync(0xffffffffu, w, 2 * k);
+            const float wb = __shfl_sync(0xffffffffu, w, 2 * k + 1);
+            bool out = false;
 #pragma unroll
-            for (int k = 0; k < GROUP; ++k) s.a[k][32 * i + lane] = v[i][k];
-          if (lane < 2 * GROUP) reinterpret_cast<float*>(s.w)[lane] = w;
+            for (int i = 0; i < 4; ++i) {
+              s.a[k][32 * i + lane] = v[i][k];
+              out |= 32 * i + lane < t.valid &&
+                     !(scales_fit(v[i][k], wa) && scales_fit(v[i][k], wb));
+            }
+            out = __any_sync(0xffffffffu, out);
+            if (lane == k) far = out;
+          }
+          if (lane < 2 * GROUP) reinterpret_cast<float*>(&s.w[lane >> 1])[lane & 1] = w;
+          if (lane < GROUP) s.w[lane].z = far ? 1.f : 0.f;
           if (lane == 0) {
             s.e = t.e; s.nb = t.nb; s.row0 = t.row0; s.valid = t.valid;
           }
@@ -589,7 +628,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
         const float sa = slots[slot].a[k][r_in_tile];
-        const float2 sw = slots[slot].w[k];
+        const float4 sw = slots[slot].w[k];
+        float m0 = sa * sw.x, m1 = sa * sw.y, f0 = 1.f, f1 = 1.f;
+        const bool far = sw.z != 0.f;  // warp-uniform, and rare
+        if (far) {
+          const float2 q0 = far_scales(sa, sw.x), q1 = far_scales(sa, sw.y);
+          m0 = q0.x; f0 = q0.y; m1 = q1.x; f1 = q1.y;
+        }
         if (!__all_sync(0xffffffffu, ready)) {
           ok = wait_inline(tfull_bar(acc), acc_phase, abort_flag, tmo);
           ok = __all_sync(0xffffffffu, ok);
@@ -607,9 +652,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ld32(tb + 32, r1);
           wait_ld(r0);
           pass_regs(r1);
-          promote32(c, r0, sa * sw.x);
+          if (far) { scale32(r0, f0); scale32(r1, f0); }
+          promote32(c, r0, m0);
           ld32(tb + 128, r0);
-          promote32(c + 32, r1, sa * sw.x);
+          promote32(c + 32, r1, m0);
           ld32(tb + 160, r1);
           wait_ld(r0);
           pass_regs(r1);
@@ -626,8 +672,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         ready = mbar_test(tfull_bar(acc), acc_phase);
         if (work) {
-          promote32(c + 64, r0, sa * sw.y);
-          promote32(c + 96, r1, sa * sw.y);
+          if (far) { scale32(r0, f1); scale32(r1, f1); }
+          promote32(c + 64, r0, m1);
+          promote32(c + 96, r1, m1);
         }
       }
       if (!ok) break;

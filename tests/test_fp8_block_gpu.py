@@ -516,3 +516,84 @@ def test_refusals():
         quantize_fp8_block(torch.zeros(4, 256, device="cuda", dtype=torch.float16), 1)
     with pytest.raises(RuntimeError):
         dequantize_fp8_block(a, sa[:, :1], 1)
+
+
+def small_codes(shape, top, g):
+    """Random nonzero codes of both signs up to `top`."""
+    c = torch.randint(1, top + 1, shape, generator=g, device="cuda", dtype=torch.uint8)
+    return c | torch.randint(0, 2, shape, generator=g, device="cuda", dtype=torch.uint8) << 7
+
+
+def scales_near(shape, e, g):
+    return torch.ldexp(1 + torch.rand(shape, generator=g, device="cuda"), torch.tensor(e, device="cuda"))
+
+
+# Powers of two of the scales: products among the subnormals, below them, above the
+# largest number, each with sums that bring the result back among the numbers
+FAR_SCALES = [(-126, -14), (-14, -126), (-70, -72), (-126, -126), (70, 60), (120, 10), (10, 117),
+              (-126, 126)]
+
+
+@pytest.mark.parametrize("ea,ew", FAR_SCALES)
+@pytest.mark.parametrize("M,N,K,E", [(1, 256, 256, 0), (5, 200, 384, 0), (300, 4096, 272, 0),
+                                     (140, 272, 512, 3), (3000, 2048, 128, 0)])
+def test_scale_products_out_of_range(M, N, K, E, ea, ew):
+    # the result of scales whose product no normal fp32 number holds is as exact as
+    # any other, and a sum of zero stays zero. Beside the bound above, an addition
+    # rounds among the subnormals by 2^-150, and the output by half its own smallest
+    g = gen(M + N)
+    kb, nb = ceil(K, BLK), ceil(N, BLK)
+    top = 3 if ea + ew > 0 else 126               # 3 * 2^-9, or the largest code
+    a, w = small_codes((M, K), top, g), small_codes((max(1, E), N, K), top, g)
+    sa, sw = scales_near((M, kb), ea, g), scales_near((max(1, E), nb, kb), ew, g)
+    a[0] = 0
+    sa[1::2, 0] = 1.0                             # beside blocks of ordinary scales
+    if kb > 1:
+        sw[:, 0, -1] = 1.0
+    offsets, cuts = None, None
+    if E:
+        cuts = [0, 10, 10, M]
+        offsets = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+    else:
+        w, sw = w[0], sw[0]
+    want, mag = product(a, sa, w, sw, cuts)
+    for dtype in (torch.float32, torch.bfloat16):
+        info = torch.finfo(dtype)
+        got = matmul_fp8_block(a, sa, w, sw, offsets=offsets, out_dtype=dtype)
+        bound = (sum_eps(K) * mag * (1 + info.eps / 2) + info.eps / 2 * want.abs()
+                 + kb * 2.0 ** -150 + info.smallest_normal * info.eps / 2)
+        fits = mag * (1 + sum_eps(K)) < info.max  # no partial sum overflows
+        assert fits.any() and torch.isfinite(got[fits]).all()
+        assert ((got.double() - want).abs() <= bound)[fits].all()
+        assert (got[0] == 0).all()
+    assert moe_get_device_status() == 0
+
+
+@pytest.mark.parametrize("M", [3, 200, 2500])
+@pytest.mark.parametrize("ea,eg,eu,top", [(-100, -44, 110, 126), (90, 40, -92, 3), (-30, 30, 2, 126)])
+def test_swiglu_scale_products_out_of_range(ea, eg, eu, top, M):
+    N, K = 272, 384
+    gn = gen(M)
+    a, wg, wu = small_codes((M, K), top, gn), small_codes((N, K), top, gn), small_codes((N, K), top, gn)
+    sa, sg, su = (scales_near(s, e, gn) for s, e in (((M, 3), ea), ((3, 3), eg), ((3, 3), eu)))
+    codes, scales = swiglu_fp8_block(a, sa, wg, wu, sg, su)
+    check_swiglu(codes, scales, *swiglu_reference(a, sa, wg, sg, wu, su))
+
+
+def test_scales_of_zero_and_infinity():
+    # a scale of zero makes its blocks zero; an infinite one makes inf, or NaN of a zero sum
+    a, sa, w, sw = operands(70, 256, 512, 0, seed=9)
+    sa0 = sa.clone()
+    sa0[:, 1] = 0.0
+    a0 = a.clone()
+    a0[:, 128:256] = 0
+    assert torch.equal(matmul_fp8_block(a, sa0, w, sw, out_dtype=torch.float32),
+                       matmul_fp8_block(a0, sa, w, sw, out_dtype=torch.float32))
+    sa1 = sa.clone()
+    sa1[3, 1] = float("inf")
+    got = matmul_fp8_block(a, sa1, w, sw, out_dtype=torch.float32)
+    clean = matmul_fp8_block(a, sa, w, sw, out_dtype=torch.float32)
+    assert torch.isinf(got[3]).all()
+    assert torch.isnan(matmul_fp8_block(a0, sa1, w, sw)[3]).all()
+    keep = [i for i in range(70) if i != 3]
+    assert torch.equal(got[keep], clean[keep])
