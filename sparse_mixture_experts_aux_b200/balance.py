@@ -5,6 +5,7 @@ from __future__ import annotations
 from typing import Optional
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 from torch.autograd.function import once_differentiable
 
 from . import _lib, streams
@@ -20,6 +21,12 @@ def _need(name: str, t: torch.Tensor, dtype, shape, dev) -> None:
         raise RuntimeError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise RuntimeError(f"{name} must be contiguous")
+
+
+def _no_tangent(where: str, *tensors) -> None:
+    for t in tensors:
+        if unpack_dual(t).tangent is not None:
+            raise RuntimeError(f"{where} has no forward-mode derivative: a tangent would be lost")
 
 
 def _args(logits, k, gate_mode, token_mask, cu_seqlens):
@@ -88,6 +95,7 @@ def balance_loss_backward(dloss: torch.Tensor, logits: torch.Tensor, counts: tor
     the call behind balance_loss's autograd, for programs that chain gradients
     themselves (it touches no autograd state, so it can be captured in a graph).
     """
+    _no_tangent("balance_loss_backward", dloss, logits)
     T, E, S, fields = _args(logits, int(k), gate_mode, token_mask, cu_seqlens)
     dev = logits.device
     _need("dloss", dloss, torch.float32, (S,), dev)
@@ -133,7 +141,8 @@ def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, gate_mode: int = 
 
     Returns (loss fp32 [S], counts int32 [S, E], tokens int32 [S]); S = 1 without
     cu_seqlens. counts are the routed assignments per expert, tokens the tokens
-    that count; neither carries a gradient. The loss is raw: scale it by the
+    that count; neither carries a gradient. Reverse mode only, once: a tangent of
+    forward mode is refused. The loss is raw: scale it by the
     trainer's weight, and average it over sequences if there are several.
 
     logits [T, E] fp32 or bf16, rows may be strided: what the softmax of the layer
@@ -148,6 +157,7 @@ def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, gate_mode: int = 
     torch.cuda.stream). The inputs must be ready there, and the results are: wait
     for it before they are used elsewhere. Both may be dropped at any time.
     """
+    _no_tangent("balance_loss", logits)
     if torch.is_grad_enabled() and logits.requires_grad:
         if stream is not None:
             raise RuntimeError("balance_loss with a gradient runs on the current stream: "

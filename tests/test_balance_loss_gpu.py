@@ -431,3 +431,23 @@ def test_rows_far_from_zero(E, gate_mode, dtype):
         logits[4 * i + 1] = (logits[4 * i + 1].float() + v).clamp(-top, top).to(dtype)
         logits[4 * i + 2, 3] = v                  # one among ordinary ones
     check(logits, idx, gate_mode, spread=100.0)
+
+
+def test_forward_mode_is_refused():
+    # a dual tensor needs no gradient by its own account; its tangent must not vanish
+    import torch.autograd.forward_ad as fwAD
+    logits, idx = draw(16, 8, 2)
+    loss, counts, tokens = balance_loss(logits, idx)
+    one = torch.ones(1, device="cuda")
+    with fwAD.dual_level():
+        for t in (logits, logits.clone().requires_grad_(True)):
+            dual = fwAD.make_dual(t, torch.ones_like(logits))
+            with pytest.raises(RuntimeError):
+                balance_loss(dual, idx)
+            with pytest.raises(RuntimeError):
+                balance_loss_backward(one, dual, counts, tokens, 2)
+        with pytest.raises(RuntimeError):
+            balance_loss_backward(fwAD.make_dual(one, one), logits, counts, tokens, 2)
+        assert torch.equal(balance_loss(logits, idx)[0], loss)
+    with pytest.raises(RuntimeError):
+        torch.func.jvp(lambda r: balance_loss(r, idx)[0], (logits,), (torch.ones_like(logits),))
