@@ -455,8 +455,9 @@ MOE_API moe_status moe_forward_no_alloc(const moe_dims* dims,
  * Masked tokens, and tokens outside every sequence, count nowhere, whatever
  * their logits hold, and get zero gradients. A row whose logits are all -inf has
  * p = 0; NaN gives NaN (as does +inf under the softmax).
- * Sums are fp32 over at most 1/148 of the batch, fp64 beyond, in a fixed order:
- * the same inputs give the same bits. Limits: 1 <= k <= 32, k <= E <= 1024,
+ * Sums of probabilities are fp32 over at most 64 rows and fp64 beyond, each part of
+ * a long sequence rounded once more to fp32, in a fixed order: the same inputs give
+ * the same bits. Limits: 1 <= k <= 32, k <= E <= 1024,
  * T <= 2^30, T k < 2^31, num_seqs E < 2^31.
  */
 typedef struct {

@@ -18,7 +18,12 @@
 // much (it needs f, a count over the whole sequence). A row's softmax stays in the registers of one group of lanes.
 // Determinism: every sum has a fixed order (lane, then warp, then chunk);
 // counts are integers. The probability sums of a warp are fp32 over at most
-// one chunk of a sequence; everything above is fp64.
+// WARP_ROWS rows; everything above is added in fp64, and rounded once to fp32
+// where a block leaves its sum of a sequence to balance_finish_kernel. All terms
+// are positive, so P is off by at most WARP_ROWS + 3 half ulps beside the
+// probabilities' own error, however long the batch. (Sums left in fp64 would save
+// one of the 67 and cost that kernel twice the bytes: 13831 tokens, 475 experts,
+// 2 sequences 44 -> 51 us both ways.)
 #pragma once
 #include "common.cuh"
 #include "router.cuh"
@@ -184,7 +189,12 @@ __device__ __forceinline__ float loss_of(double dot, int n, int E, int k) {
 // times ROWS_AT_ONCE at a time. The block walks the sequences that its chunk
 // meets; each leaves its sums in slot (chunk + sequence), which no other pair has, or, when the
 // sequence lies inside the chunk, its results at once.
-// Dynamic shared memory: float psum[warps][E], int32 counts[E].
+// The fp32 sums of a warp's rows end after WARP_ROWS of them, so that their error
+// (at most WARP_ROWS half ulps) does not grow with the batch; a chunk holds more
+// than one such span of rows from some 300 thousand tokens on (32 warps a block).
+// Dynamic shared memory: double total[E] (the spans before the last), float
+// psum[warps][E], int32 counts[E].
+constexpr int WARP_ROWS = 64;
 template <typename TL, int G, int NV, bool SIG>
 __global__ void __launch_bounds__(NV > 8 ? 8192 / NV : 1024) balance_kernel(const BalParams p) {
   pdl_wait();
@@ -192,7 +202,8 @@ __global__ void __launch_bounds__(NV > 8 ? 8192 / NV : 1024) balance_kernel(cons
   extern __shared__ __align__(16) uint8_t bal_smem[];
   constexpr int U = ROWS_AT_ONCE<NV>, PER = 32 / G * U;
   const int THREADS = blockDim.x, WARPS = THREADS / 32;
-  float* s_psum = reinterpret_cast<float*>(bal_smem);
+  double* s_total = reinterpret_cast<double*>(bal_smem);
+  float* s_psum = reinterpret_cast<float*>(s_total + p.E);
   int32_t* s_cnt = reinterpret_cast<int32_t*>(s_psum + (size_t)WARPS * p.E);
   __shared__ double s_red[32];
   __shared__ int s_n;
@@ -214,16 +225,19 @@ __global__ void __launch_bounds__(NV > 8 ? 8192 / NV : 1024) balance_kernel(cons
   for (int s = first_seq_past(p.cu, p.S, c0); s < p.S; ++s) {
     const int qb = seq_begin(p.cu, s, p.T), qe = seq_end(p.cu, s, p.T);
     if (qb >= c1) break;
-    const int b = max(qb, c0), e = min(qe, c1);
+    int b = max(qb, c0), e = min(qe, c1);
     if (b >= e) continue;
+    const int last = e, span = WARPS * WARP_ROWS;
+    const bool spans = e - b > span;
     __syncthreads();
-    for (int i = threadIdx.x; i < p.E; i += THREADS) s_cnt[i] = 0;
+    for (int i = threadIdx.x; i < p.E; i += THREADS) {
+      s_cnt[i] = 0;
+      if (spans) s_total[i] = 0.0;
+    }
     if (threadIdx.x == 0) s_n = 0;
     __syncthreads();
     float ps[NV], next[U][NV];
     bool next_live[U];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) ps[i] = 0.f;
     int mine = 0;
     // the next rows' logits are loaded before these are worked on
     auto load = [&](int t0) {
@@ -234,41 +248,54 @@ __global__ void __launch_bounds__(NV > 8 ? 8192 / NV : 1024) balance_kernel(cons
         load_row<TL, G, NV>(logits + (int64_t)t * p.ld, next_live[u], sub, p.E, next[u]);
       }
     };
-    load(b + warp * PER);
-    for (int t0 = b + warp * PER; t0 < e; t0 += WARPS * PER) {
-      float v[U][NV], slope[U][NV], inv[U];
-      bool live[U];
-      int chosen[U];
+    for (;; b = e) {  // spans of rows, mostly one
+      e = min(last, b + span);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        live[u] = next_live[u];
+      for (int i = 0; i < NV; ++i) ps[i] = 0.f;
+      load(b + warp * PER);
+      for (int t0 = b + warp * PER; t0 < e; t0 += WARPS * PER) {
+        float v[U][NV], slope[U][NV], inv[U];
+        bool live[U];
+        int chosen[U];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) v[u][i] = next[u][i];
-        const int t = t0 + u * (32 / G) + grp;
-        chosen[u] = live[u] && sub < p.k ? p.idx[(int64_t)t * p.k + sub] : -1;
-      }
-      load(t0 + WARPS * PER);
-      row_terms<G, NV, U, SIG>(v, slope, inv);
+        for (int u = 0; u < U; ++u) {
+          live[u] = next_live[u];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (!live[u]) continue;
-        const int t = t0 + u * (32 / G) + grp;
-        if ((unsigned)chosen[u] < (unsigned)p.E) atomicAdd(&s_cnt[chosen[u]], 1);
-        for (int j = sub + G; j < p.k; j += G) {
-          const int x = p.idx[(int64_t)t * p.k + j];
-          if ((unsigned)x < (unsigned)p.E) atomicAdd(&s_cnt[x], 1);
+          for (int i = 0; i < NV; ++i) v[u][i] = next[u][i];
+          const int t = t0 + u * (32 / G) + grp;
+          chosen[u] = live[u] && sub < p.k ? p.idx[(int64_t)t * p.k + sub] : -1;
         }
-        mine += sub == 0;
+        load(t0 + WARPS * PER);
+        row_terms<G, NV, U, SIG>(v, slope, inv);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) ps[i] = fmaf(v[u][i], inv[u], ps[i]);
+        for (int u = 0; u < U; ++u) {
+          if (!live[u]) continue;
+          const int t = t0 + u * (32 / G) + grp;
+          if ((unsigned)chosen[u] < (unsigned)p.E) atomicAdd(&s_cnt[chosen[u]], 1);
+          for (int j = sub + G; j < p.k; j += G) {
+            const int x = p.idx[(int64_t)t * p.k + j];
+            if ((unsigned)x < (unsigned)p.E) atomicAdd(&s_cnt[x], 1);
+          }
+          mine += sub == 0;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) ps[i] = fmaf(v[u][i], inv[u], ps[i]);
+        }
       }
+      // the groups of a warp hold the same experts: add them up
+#pragma unroll
+      for (int o = G; o < 32; o <<= 1) ps[0] += __shfl_xor_sync(0xffffffffu, ps[0], o);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (lane < G && sub + G * i < p.E) s_psum[(size_t)warp * p.E + sub + G * i] = ps[i];
+      if (e == last) break;
+      __syncthreads();
+      for (int i = threadIdx.x; i < p.E; i += THREADS) {
+        double acc = 0.0;
+        for (int w = 0; w < WARPS; ++w) acc += (double)s_psum[(size_t)w * p.E + i];
+        s_total[i] += acc;
+      }
+      __syncthreads();
     }
-    // the groups of a warp hold the same experts: add them up
-#pragma unroll
-    for (int o = G; o < 32; o <<= 1) ps[0] += __shfl_xor_sync(0xffffffffu, ps[0], o);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (lane < G && sub + G * i < p.E) s_psum[(size_t)warp * p.E + sub + G * i] = ps[i];
     if (mine) atomicAdd(&s_n, mine);
     __syncthreads();
     const bool whole = qb >= c0 && qe <= c1;
@@ -279,6 +306,7 @@ __global__ void __launch_bounds__(NV > 8 ? 8192 / NV : 1024) balance_kernel(cons
       double acc = 0.0;
 #pragma unroll 8
       for (int w = 0; w < WARPS; ++w) acc += (double)s_psum[(size_t)w * p.E + i];
+      if (spans) acc += s_total[i];
       const int c = s_cnt[i];
       if (whole) {
         p.counts[(size_t)s * p.E + i] = c;

@@ -1229,7 +1229,7 @@ void launch_balance(const moe::bal::BalParams& p, cudaStream_t st) {
     const unsigned most = NV > 8 ? 8192 / NV : 1024;                                         \
     const unsigned threads = p.chunk <= MOE_BALANCE_SMALL_T ? 256 : most;                    \
     launch_pdl(moe::bal::balance_kernel<TL, G, NV, SIG>, grid, threads,                      \
-               static_cast<size_t>(p.E) * 4 * (threads / 32 + 1), st, p);                    \
+               static_cast<size_t>(p.E) * (4 * (threads / 32 + 1) + 8), st, p);              \
   } while (0)
   MOE_BAL_DISPATCH(p.E, MOE_BAL_FWD);
 #undef MOE_BAL_FWD

@@ -451,3 +451,36 @@ def test_forward_mode_is_refused():
         assert torch.equal(balance_loss(logits, idx)[0], loss)
     with pytest.raises(RuntimeError):
         torch.func.jvp(lambda r: balance_loss(r, idx)[0], (logits,), (torch.ones_like(logits),))
+
+
+@pytest.mark.parametrize("T,E", [(1 << 26, 8), (1 << 24, 100), (1 << 22, 600)])
+def test_rounding_of_the_sums_does_not_grow_with_the_batch(T, E):
+    # equal rows: the mean of T probabilities is the probability, which a batch of one
+    # row gives with the same rounding. 64 fp32 additions, two levels of a warp's own,
+    # the probability's and the result's rounding are what may differ
+    row = torch.randn(1, E, generator=torch.Generator().manual_seed(16)).to(torch.bfloat16).cuda()
+    idx = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    one = balance_loss(row, idx[:1])[0].item()
+    loss, counts, tokens = balance_loss(row.expand(T, E).contiguous(), idx)
+    assert counts[0, 0].item() == T and tokens.item() == T
+    assert abs(loss.item() - one) <= 68 * 2.0 ** -24 * one
+
+
+@pytest.mark.parametrize("T,E,k", [(700_001, 12, 2), (350_003, 200, 3), (80_007, 600, 2)])
+def test_chunks_of_several_spans(T, E, k):
+    # sequences that hold several spans of rows, end inside one, or inside a chunk
+    g = torch.Generator(device="cuda").manual_seed(18)
+    logits = torch.randn(T, E, generator=g, device="cuda") * 2
+    idx = torch.topk(logits, k, dim=1).indices.int()
+    mask = torch.rand(T, generator=g, device="cuda") < 0.8
+    cuts = [0, T // 2 + 5, T // 2 + 700, T - 3]
+    loss, counts, tokens = balance_loss(logits, idx, token_mask=mask,
+                                        cu_seqlens=torch.tensor(cuts, dtype=torch.int32, device="cuda"))
+    for s, (b, e) in enumerate(zip(cuts[:-1], cuts[1:])):
+        live = mask[b:e]
+        n = int(live.sum())
+        c = torch.bincount(idx[b:e][live].reshape(-1).long(), minlength=E)
+        p = torch.softmax(logits[b:e][live].double(), dim=1).mean(dim=0)
+        want = float(E * (c.double() / (n * k) * p).sum())
+        assert tokens[s].item() == n and torch.equal(counts[s].long(), c)
+        assert abs(loss[s].item() - want) <= (eps_p(E, 24.0) + 66 * 2.0 ** -24 + 2.0 ** -23) * want
