@@ -5,7 +5,7 @@ from __future__ import annotations
 from typing import Optional
 
 import torch
-from torch.autograd.forward_ad import unpack_dual
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _lib, streams
@@ -24,8 +24,10 @@ def _need(name: str, t: torch.Tensor, dtype, shape, dev) -> None:
 
 
 def _no_tangent(where: str, *tensors) -> None:
+    if forward_ad._current_level < 0:  # no dual tensors outside a dual level
+        return
     for t in tensors:
-        if unpack_dual(t).tangent is not None:
+        if forward_ad.unpack_dual(t).tangent is not None:
             raise RuntimeError(f"{where} has no forward-mode derivative: a tangent would be lost")
 
 
