@@ -21,6 +21,7 @@
 #include "balance.cuh"
 #include "fp8_block.cuh"
 #include "fp8_block_gemm.cuh"
+#include "split_clusters.cuh"
 
 namespace {
 
@@ -194,7 +195,7 @@ struct DeviceInfo {
   bool ready = false;
   int num_sms = 0;
   int pair_clusters[2] = {0, 0};  // co-resident 2-CTA clusters of each pair GEMM kernel
-  int split_clusters[9] = {};     // [s]: co-resident s-CTA clusters of the block-scaled products
+  int split_clusters[moe::f8b::MAX_SPLIT + 1] = {};  // [s]: co-resident s-CTA clusters of the block-scaled products
 };
 constexpr int kMaxDevices = 64;
 DeviceInfo g_devices[kMaxDevices];
@@ -213,28 +214,25 @@ bool f8b_attr() {
                               moe::f8b::SMEM_BYTES) == cudaSuccess;
 }
 
-// Co-resident clusters of 2..8 CTAs (fewer than SMs / size where a GPC's SMs do
-// not divide: 15 of 8 on a B200).
-bool f8b_clusters(int* clusters) {
-  for (int s = 2; s <= 8; ++s) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(s));
-    cfg.blockDim = dim3(moe::f8b::NUM_THREADS);
-    cfg.dynamicSmemBytes = moe::f8b::SMEM_BYTES;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(s);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, moe::f8b::gemm_kernel<moe::f8b::MATMUL, true>, &cfg) !=
-        cudaSuccess)
-      return false;
-    clusters[s] = n;
-  }
-  return true;
+// Co-resident clusters of s CTAs (fewer than SMs / s where a GPC's SMs do not
+// divide: 15 of 8 on a B200); false when the runtime cannot say.
+bool f8b_clusters(int s, int* n) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(s));
+  cfg.blockDim = dim3(moe::f8b::NUM_THREADS);
+  cfg.dynamicSmemBytes = moe::f8b::SMEM_BYTES;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(s);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(n, moe::f8b::gemm_kernel<moe::f8b::MATMUL, true>, &cfg) ==
+      cudaSuccess)
+    return true;
+  (void)cudaGetLastError();  // or the next launch's check would report it
+  return false;
 }
 
 template <int EPI, int AR, bool Q8 = false>
@@ -392,9 +390,9 @@ moe_status device_setup(int* num_sms, int* pair_clusters = nullptr,
                              moe::rtc::SMEM_LIMIT) != cudaSuccess)
       return MOE_ERR_CUDA;
     if (!f8b_attr<moe::f8b::MATMUL, false>() || !f8b_attr<moe::f8b::MATMUL, true>() ||
-        !f8b_attr<moe::f8b::SWIGLU, false>() || !f8b_attr<moe::f8b::SWIGLU, true>() ||
-        !f8b_clusters(di.split_clusters))
+        !f8b_attr<moe::f8b::SWIGLU, false>() || !f8b_attr<moe::f8b::SWIGLU, true>())
       return MOE_ERR_CUDA;
+    moe::f8b::co_resident_clusters(f8b_clusters, di.split_clusters);
     const int rs = static_cast<int>(moe::route_smem_bytes(moe::tc::MAX_E));
     if (cudaFuncSetAttribute(moe::route_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              rs) != cudaSuccess ||
@@ -669,7 +667,7 @@ moe_status launch_f8b(moe::f8b::Params& p, int64_t rows, int K, const void* a, i
   const int64_t tiles = p.n_tiles * row_tiles;
   int cluster = 1;
   int64_t best = (tiles + num_sms - 1) / num_sms * p.k_blocks + 4;
-  for (int s = 2; s <= 8 && p.k_blocks >= 2 * s && tiles <= 4 * num_sms; ++s) {
+  for (int s = 2; s <= MAX_SPLIT && p.k_blocks >= 2 * s && tiles <= 4 * num_sms; ++s) {
     if (clusters[s] < 1) continue;
     const int64_t cost =
         (tiles + clusters[s] - 1) / clusters[s] * ((p.k_blocks + s - 1) / s + 8);

@@ -1,5 +1,9 @@
 """The balance loss and block-scaled FP8 entry points refuse bad arguments on the
 host, before anything is enqueued (no GPU)."""
+import ctypes
+import shutil
+import subprocess
+
 import pytest
 
 from sparse_mixture_experts_aux_b200 import _lib
@@ -152,3 +156,32 @@ def test_layer_format():
     st = _lib.moe_forward(dims(workspace=P, workspace_bytes=need), P, P, P, P, P, None, 8, 2, 0.0, P,
                           P, P, check=False)
     assert st == BAD                                      # no weight_scales
+
+
+SPLIT_PROBE = """
+#include "split_clusters.cuh"
+extern "C" void clusters(const int* known, const int* counts, int* out) {
+  moe::f8b::co_resident_clusters(
+      [&](int s, int* n) { *n = counts[s]; return known[s] != 0; }, out);
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_cluster_sizes_the_runtime_does_not_know_are_left_out(tmp_path):
+    # a size whose occupancy query fails is not used; it refuses no call
+    src, so = tmp_path / "probe.cpp", tmp_path / "probe.so"
+    src.write_text(SPLIT_PROBE)
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", B.CSRC, "-x", "c++",
+                    str(src), "-o", str(so)], check=True)
+    probe = ctypes.CDLL(str(so))
+    ints = ctypes.c_int * 9
+    counts = ints(0, 0, 74, 48, 36, 28, 22, 20, 15)
+    for known, want in [([1] * 9, [74, 48, 36, 28, 22, 20, 15]), ([0] * 9, [0] * 7),
+                        ([1, 1, 1, 1, 0, 1, 0, 1, 0], [74, 48, 0, 28, 0, 20, 0])]:
+        out = ints(*[7] * 9)
+        probe.clusters(ints(*known), counts, out)
+        assert list(out)[2:] == want
+    out = ints()
+    probe.clusters(ints(*[1] * 9), ints(0, 0, -1, 0, 5, 0, 0, 0, 0), out)
+    assert list(out)[2:] == [0, 0, 5, 0, 0, 0, 0]
