@@ -59,20 +59,22 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 
 struct Divisor {
   float scale;
-  uint64_t inv2, neg2;  // 1 / scale and -scale, twice each
+  uint64_t neg_inv2, scale2;  // -1 / scale and scale, twice each
   bool fast;
   __device__ __forceinline__ explicit Divisor(float s) : scale(s) {
     fast = s > 0x1p-80f && s < 0x1p100f;
     const float inv = fast ? __frcp_rn(s) : 0.f;
-    inv2 = pack2(inv, inv);
-    neg2 = pack2(-s, -s);
+    neg_inv2 = pack2(-inv, -inv);
+    scale2 = pack2(s, s);
   }
-  // codes of a / scale and b / scale
-  __device__ __forceinline__ uint32_t codes2(float a, float b) const {
+  // Codes of -a / scale and -b / scale: fp32 rounds both signs alike, and the negated
+  // form keeps a zero's sign (+0 gives -0 + -0 = -0, and -0 gives +0 + -0 = +0), where
+  // q + r y itself makes +0 of both.
+  __device__ __forceinline__ uint32_t neg_codes2(float a, float b) const {
     const uint64_t x = pack2(a, b);
     uint64_t q;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(inv2));
-    q = fma2(fma2(q, neg2, x), inv2, q);
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(neg_inv2));
+    q = fma2(fma2(q, scale2, x), neg_inv2, q);
     float lo, hi;
     asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(q));
     return e4m3x2(lo, hi);
@@ -80,7 +82,8 @@ struct Divisor {
 };
 
 __device__ __forceinline__ uint32_t encode4(const float* f, const Divisor& d) {
-  if (d.fast) return d.codes2(f[0], f[1]) | d.codes2(f[2], f[3]) << 16;
+  if (d.fast)
+    return (d.neg_codes2(f[0], f[1]) | d.neg_codes2(f[2], f[3]) << 16) ^ 0x80808080u;
   return e4m3x4_by_division(f[0], f[1], f[2], f[3], d.scale);
 }
 

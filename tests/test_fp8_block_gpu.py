@@ -597,3 +597,20 @@ def test_scales_of_zero_and_infinity():
     assert torch.isnan(matmul_fp8_block(a0, sa1, w, sw)[3]).all()
     keep = [i for i in range(70) if i != 3]
     assert torch.equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantizer_keeps_the_sign_of_zero(block_rows, dtype):
+    # zeros of both signs, and quotients that round to them, beside ordinary elements
+    # and in blocks of nothing else
+    w = torch.randn(300, 272, generator=gen(3), device="cuda").to(dtype)
+    w[::3, ::2] = -0.0
+    w[::3, 1::2] = 0.0
+    w[1::3, ::4] *= -2.0 ** -20
+    w[5] = -0.0
+    w[128:256, 128:256] = -0.0
+    codes, scales = quantize_fp8_block(w, block_rows)
+    rc, rs = reference_codes(w[None], block_rows)
+    assert (rc == 0x80).any() and (rc == 0).any()
+    assert torch.equal(scales.cpu(), rs[0]) and torch.equal(codes.cpu(), rc[0])
