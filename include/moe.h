@@ -506,7 +506,8 @@ MOE_API moe_status moe_balance_loss_backward(const moe_balance_dims* dims, const
  *          cols; a multiple of 16 bytes), matrices rows * ld apart
  *   codes  device uint8 [stack, rows, cols], dense
  *   scales device fp32 [stack, ceil(rows / block_rows), ceil(cols / 128)]
- * cols is a multiple of 16; edge blocks may be smaller than 128.
+ * cols is a multiple of 16; edge blocks may be smaller than 128. No matrices or no
+ * rows: nothing is written, and the pointers may be null.
  */
 MOE_API moe_status moe_quantize_fp8_block(const void* w, int32_t dtype, int64_t stack,
                                           int64_t rows, int32_t cols, int64_t ld,

@@ -1574,12 +1574,15 @@ moe_status moe_balance_loss_backward(const moe_balance_dims* dims, const float* 
 moe_status moe_quantize_fp8_block(const void* w, int32_t dtype, int64_t stack, int64_t rows,
                                   int32_t cols, int64_t ld, int32_t block_rows, uint8_t* codes,
                                   float* scales, void* stream) {
-  if (w == nullptr || codes == nullptr || scales == nullptr || stack < 0 || rows < 0 || cols < 1 ||
-      cols % 16 != 0 || (dtype != MOE_BF16 && dtype != MOE_F32) ||
-      (block_rows != 1 && block_rows != moe::f8b::BLK) || !aligned(scales, 4) || !aligned(w, 16) ||
-      !aligned(codes, 16) || (ld != 0 && (ld < cols || ld % (dtype == MOE_BF16 ? 8 : 4) != 0)))
+  if (stack < 0 || rows < 0 || cols < 1 || cols % 16 != 0 ||
+      (dtype != MOE_BF16 && dtype != MOE_F32) ||
+      (block_rows != 1 && block_rows != moe::f8b::BLK) ||
+      (ld != 0 && (ld < cols || ld % (dtype == MOE_BF16 ? 8 : 4) != 0)))
     return MOE_ERR_INVALID_ARG;
   if (stack == 0 || rows == 0) return MOE_OK;
+  if (w == nullptr || codes == nullptr || scales == nullptr || !aligned(scales, 4) ||
+      !aligned(w, 16) || !aligned(codes, 16))
+    return MOE_ERR_INVALID_ARG;
   if (ld == 0) ld = cols;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t kb = (cols + moe::f8b::BLK - 1) / moe::f8b::BLK;
@@ -1616,11 +1619,13 @@ moe_status moe_quantize_fp8_block(const void* w, int32_t dtype, int64_t stack, i
 moe_status moe_dequantize_fp8_block(const uint8_t* codes, const float* scales, int64_t stack,
                                     int64_t rows, int32_t cols, int32_t block_rows, float* out,
                                     void* stream) {
-  if (codes == nullptr || scales == nullptr || out == nullptr || stack < 0 || rows < 0 ||
-      cols < 1 || cols % 16 != 0 || (block_rows != 1 && block_rows != moe::f8b::BLK) ||
-      !aligned(codes, 16) || !aligned(out, 16) || !aligned(scales, 4))
+  if (stack < 0 || rows < 0 || cols < 1 || cols % 16 != 0 ||
+      (block_rows != 1 && block_rows != moe::f8b::BLK))
     return MOE_ERR_INVALID_ARG;
   if (stack == 0 || rows == 0) return MOE_OK;
+  if (codes == nullptr || scales == nullptr || out == nullptr || !aligned(codes, 16) ||
+      !aligned(out, 16) || !aligned(scales, 4))
+    return MOE_ERR_INVALID_ARG;
   const int64_t blocks = (stack * rows * (cols / 16) + 255) / 256;
   launch_pdl(moe::f8b::dequantize_blocks_kernel, static_cast<unsigned>(blocks < 16384 ? blocks : 16384),
              256, 0, static_cast<cudaStream_t>(stream), codes, scales, stack, rows, cols, block_rows,

@@ -6,6 +6,7 @@ must be ready there, and the results are: wait for it before they are used
 elsewhere. Both may be dropped at any time."""
 from __future__ import annotations
 
+import math
 from typing import Optional
 
 import torch
@@ -19,6 +20,10 @@ _CODES = (torch.uint8, torch.float8_e4m3fn)
 
 def _ceil(n: int, b: int) -> int:
     return -(-n // b)
+
+
+def _stack(t: torch.Tensor) -> int:
+    return math.prod(t.shape[:-2])
 
 
 def quantize_fp8_block(w: torch.Tensor, block_rows: int = 128, stream=None):
@@ -38,9 +43,6 @@ def quantize_fp8_block(w: torch.Tensor, block_rows: int = 128, stream=None):
     ld = w.stride(-2) if w.dim() == 2 and rows > 1 else cols
     if not w.is_contiguous() and (w.dim() > 2 or (cols > 1 and w.stride(-1) != 1) or ld < cols):
         raise RuntimeError("w must be contiguous (the rows of a matrix may be strided)")
-    stack = 1
-    for n in w.shape[:-2]:
-        stack *= n
     dev = w.device
     handle, side = streams.run_on(stream, dev)
     with streams.on(dev, side):
@@ -48,10 +50,8 @@ def quantize_fp8_block(w: torch.Tensor, block_rows: int = 128, stream=None):
         srows = rows if block_rows == 1 else _ceil(rows, max(1, block_rows))
         scales = torch.empty((*w.shape[:-2], srows, _ceil(cols, 128)), dtype=torch.float32,
                              device=dev)
-        if w.numel() == 0 and cols > 0:
-            return codes, scales
-        rc = _lib.moe_quantize_fp8_block(w, dtype_code(w.dtype), stack, rows, cols, ld, block_rows,
-                                         codes, scales, handle)
+        rc = _lib.moe_quantize_fp8_block(w, dtype_code(w.dtype), _stack(w), rows, cols, ld,
+                                         block_rows, codes, scales, handle)
     if rc != _lib.MOE_OK:
         raise _lib.MoeError(rc, "moe_quantize_fp8_block")
     streams.lend(side, w)
@@ -71,10 +71,8 @@ def dequantize_fp8_block(codes: torch.Tensor, scales: torch.Tensor, block_rows: 
     handle, side = streams.run_on(stream, dev)
     with streams.on(dev, side):
         out = torch.empty(codes.shape, dtype=torch.float32, device=dev)
-        if codes.numel() == 0 and cols > 0:
-            return out
-        rc = _lib.moe_dequantize_fp8_block(codes, scales, codes.numel() // (rows * cols), rows, cols,
-                                           block_rows, out, handle)
+        rc = _lib.moe_dequantize_fp8_block(codes, scales, _stack(codes), rows, cols, block_rows, out,
+                                           handle)
     if rc != _lib.MOE_OK:
         raise _lib.MoeError(rc, "moe_dequantize_fp8_block")
     streams.lend(side, codes, scales)

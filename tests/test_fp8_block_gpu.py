@@ -614,3 +614,23 @@ def test_quantizer_keeps_the_sign_of_zero(block_rows, dtype):
     rc, rs = reference_codes(w[None], block_rows)
     assert (rc == 0x80).any() and (rc == 0).any()
     assert torch.equal(scales.cpu(), rs[0]) and torch.equal(codes.cpu(), rc[0])
+
+
+def test_empty_matrices():
+    def empty(*shape, dtype=torch.float32):
+        return torch.empty(*shape, dtype=dtype, device="cuda")
+
+    for shape, block_rows, scales in [((0, 256), 1, (0, 2)), ((0, 256), 128, (0, 2)),
+                                      ((0, 5, 144), 1, (0, 5, 2)), ((3, 0, 16), 128, (3, 0, 1))]:
+        c, s = quantize_fp8_block(empty(*shape), block_rows)
+        assert c.shape == shape and s.shape == scales
+        assert dequantize_fp8_block(c, s, block_rows).shape == shape
+    # refused with and without rows: no columns, and sizes that are refused of any matrix
+    for rows in (0, 4):
+        for cols, block_rows in ((0, 1), (0, 128), (24, 1)):
+            with pytest.raises(RuntimeError):
+                quantize_fp8_block(empty(rows, cols), block_rows)
+            with pytest.raises(RuntimeError):
+                dequantize_fp8_block(empty(rows, cols, dtype=torch.uint8),
+                                     empty(rows if block_rows == 1 else ceil(rows, 128), ceil(cols, 128)),
+                                     block_rows)

@@ -185,3 +185,12 @@ def test_cluster_sizes_the_runtime_does_not_know_are_left_out(tmp_path):
     out = ints()
     probe.clusters(ints(*[1] * 9), ints(0, 0, -1, 0, 5, 0, 0, 0, 0), out)
     assert list(out)[2:] == [0, 0, 5, 0, 0, 0, 0]
+
+
+def test_sizes_are_checked_where_there_is_nothing_to_do():
+    for stack, rows in ((0, 4), (1, 0)):
+        assert _lib.moe_quantize_fp8_block(0, 0, stack, rows, 256, 0, 1, 0, 0) == _lib.MOE_OK
+        assert _lib.moe_dequantize_fp8_block(0, 0, stack, rows, 256, 1, 0) == _lib.MOE_OK
+        for cols, block_rows in ((0, 1), (24, 1), (256, 64)):
+            assert _lib.moe_quantize_fp8_block(0, 0, stack, rows, cols, 0, block_rows, 0, 0) == BAD
+            assert _lib.moe_dequantize_fp8_block(0, 0, stack, rows, cols, block_rows, 0) == BAD
