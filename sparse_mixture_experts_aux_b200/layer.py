@@ -103,10 +103,17 @@ def forward(x: torch.Tensor, W_r: torch.Tensor, W_g: torch.Tensor, W_u: torch.Te
         raise RuntimeError("act_fp8 needs FP8 (uint8) weights")
     if weight_block_scales is not None and (act_fp8 or W_g.dtype != torch.uint8):
         raise RuntimeError("weight_block_scales go with MXFP4 (uint8) weights, without act_fp8")
+    if W_g.dtype not in (x.dtype, torch.uint8) or not W_g.dtype == W_u.dtype == W_d.dtype:
+        raise RuntimeError("W_g, W_u and W_d must all be of x's dtype, or all uint8 codes")
     if fp8_block:
         if W_g.dtype != torch.uint8 or act_fp8 or weight_block_scales is not None:
             raise RuntimeError("fp8_block needs uint8 weights, without act_fp8 or weight_block_scales")
-        blocks = 3 * E * (-(-x.shape[1] // 128)) * (-(-W_g.shape[1] // 128))
+        d, d_e = x.shape[1], W_g.shape[1]
+        for name, t, shape in (("W_g", W_g, (E, d_e, d)), ("W_u", W_u, (E, d_e, d)),
+                               ("W_d", W_d, (E, d, d_e))):
+            if tuple(t.shape) != shape or t.device != dev:
+                raise RuntimeError(f"{name} must be {list(shape)} on {dev}, got {list(t.shape)} on {t.device}")
+        blocks = 3 * E * (-(-d // 128)) * (-(-d_e // 128))
         if weight_scales.numel() != blocks or not weight_scales.is_contiguous():
             raise RuntimeError(f"fp8_block needs {blocks} weight_scales, one after another")
     probe = _dims_for(x, W_g, d_s, router_bias, None, stream, events, routing=routing,

@@ -189,3 +189,22 @@ def test_refusals():
     with pytest.raises(RuntimeError):
         forward(inp["x"].float(), *args[1:], k=2, weight_scales=q["scales"], fp8_block=True)
     assert ceil(w.d, 128) == 4
+
+
+def test_weights_of_other_shapes_and_types_are_refused():
+    w = CASES[2]                                  # d = 320, d_e = 448
+    inp = make_inputs(w, device="cuda")
+    q = quantised(inp)
+    names = ("W_g", "W_u", "W_d")
+    good = [q[n] for n in names]
+    kw = dict(k=w.k, weight_scales=q["scales"], fp8_block=True)
+    for i in range(3):
+        for bad in (good[i][:-1], good[i][:, :-1].contiguous(), good[i].transpose(1, 2).contiguous(),
+                    good[i][0], inp[names[i]], good[i].view(torch.float8_e4m3fn)):
+            args = list(good)
+            args[i] = bad
+            with pytest.raises(RuntimeError):
+                forward(inp["x"], inp["W_r"], *args, **kw)
+    # codes of another type are not read as numbers of x's type, whatever the format
+    with pytest.raises(RuntimeError):
+        forward(inp["x"], inp["W_r"], *[t.view(torch.float8_e4m3fn) for t in good], k=w.k)
