@@ -208,3 +208,25 @@ def test_weights_of_other_shapes_and_types_are_refused():
     # codes of another type are not read as numbers of x's type, whatever the format
     with pytest.raises(RuntimeError):
         forward(inp["x"], inp["W_r"], *[t.view(torch.float8_e4m3fn) for t in good], k=w.k)
+
+
+def test_group_limited_selection():
+    # experts chosen from 2 of 4 groups: the layer's own choices and gates, and y
+    # within the format's roundings of the bf16 layer (see test_stages)
+    w = Workload("groups", 150, 256, 32, 256, 4, seed=8, gate_mode=2, selection_bias=True)
+    inp = make_inputs(w, device="cuda")
+    q = quantised(inp)
+    ws, ws2 = Workspace(), Workspace()
+    kw = dict(n_group=4, topk_group=2)
+    y, aux, counts = run(w, inp, q, ws, **kw)
+    y2, aux2, counts2 = forward(inp["x"], inp["W_r"], inp["W_g"], inp["W_u"], inp["W_d"], k=w.k,
+                                router_bias=inp["router_bias"], selection_bias=inp["selection_bias"],
+                                gate_mode=2, workspace=ws2, **kw)
+    v = routing_views(ws.buf, inp["x"], q["W_g"], w.E, w.k, fp8_block=True)
+    v2 = routing_views(ws2.buf, inp["x"], inp["W_g"], w.E, w.k)
+    assert torch.equal(v["topk_idx"], v2["topk_idx"]) and torch.equal(v["gates"], v2["gates"])
+    assert torch.equal(counts, counts2) and torch.equal(aux, aux2)
+    groups = v["topk_idx"] // 8
+    assert max(len(set(r)) for r in groups.tolist()) <= 2
+    rel = float((y.double() - y2.double()).norm() / y2.double().norm())
+    assert rel <= (2 * 1.28 ** 2 + 4) ** 0.5 * 2.0 ** -4 / 3 ** 0.5
