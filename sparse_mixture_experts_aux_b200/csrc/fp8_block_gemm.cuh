@@ -75,9 +75,9 @@ constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * SCALE_SLOTS + 4;
 static_assert(8 * NUM_BARS + 8 <= BAR_BYTES, "barriers, TMEM address, abort flag");
 struct ScaleSlot {
   float a[GROUP][BM];            // the rows' scales
-  float4 w[GROUP];               // the weight scales of the tile's two halves; z: some product
-                                 // of a row's scale with one of them is no normal number
+  float2 w[GROUP];               // the weight scales of the tile's two halves
   int e, nb, row0, valid;        // the tile, in its first group
+  int far[4];                    // [0]: scales whose product may be no normal number
 };
 constexpr int MAX_BYTES = 2 * 2 * BM * 4;  // SWIGLU: row maxima of the two half tiles, double-buffered
 constexpr int STAGING_BYTES = EPI_WARPS * 2048;  // 32 rows of 64 output bytes a warp
@@ -155,30 +155,50 @@ __device__ __forceinline__ void promote32(float* acc, const uint32_t* r, float m
 #pragma unroll
   for (int i = 0; i < 32; ++i) acc[i] = fmaf(m, __uint_as_float(r[i]), acc[i]);
 }
-// The product of two scales as fp32 holds it, and outside the normal numbers that
-// of one scale times 2^64 or of both times 2^-64; the sums then take the rest, 2^-64
-// or 2^128, first. They are exact through it: a nonzero one lies within 2^-18 ..
-// 2^25. So a scaled sum that fp32 can hold comes out as it should, where the plain
-// product would have lost bits to a subnormal, or made inf of a number and NaN of a
-// zero. What still under- or overflows here does so in the scaled sum itself.
-__device__ __forceinline__ bool scales_fit(float a, float w) {
-  const float m = fabsf(a * w);
-  return (m >= FLT_MIN && m <= FLT_MAX) || a == 0.f || w == 0.f;
-}
-__device__ __noinline__ float2 far_scales(float a, float w) {
-  const float m = a * w;
-  if (scales_fit(a, w)) return make_float2(m, 1.f);
-  if (fabsf(m) < FLT_MIN) {  // the smaller of the two is far below one
-    const bool less = fabsf(a) < fabsf(w);
-    return make_float2((less ? a : w) * 0x1p64f * (less ? w : a), 0x1p-64f);
+// Scales of 2^-62 .. 2^62 have a product that is a normal number. In a group of K
+// blocks with any other scale (flagged by the warp that fetches them) the product is
+// taken as fp32 holds it, and outside the normal numbers as that of one scale times
+// 2^64, or of both times 2^-64; the sums take the rest, 2^-64 or 2^128, first, and
+// are exact through it: a nonzero one lies within 2^-18 .. 2^25. So a scaled sum that
+// fp32 can hold comes out as it should, where the plain product would have lost bits
+// to a subnormal, or made inf of a number and NaN of a zero. What still under- or
+// overflows here does so in the scaled sum itself.
+constexpr float NEAR_LO = 0x1p-62f, NEAR_HI = 0x1p62f;
+// 64 columns of a warp's sums in TMEM times 2^-64 or 2^128 as a w asks for; returns
+// the factor that is left. In TMEM, before the sums are read, so that the code that
+// reads and adds them stays what it is. Without any of this 4736 x 4096 x 8192 takes
+// 147 us and 8192 rows over 8 experts (14336 -> 4096) 496; this way 151 and 512, the
+// corrections in registers instead 167 and 557, in a loop of their own 516 and 1710
+// (128 accumulators through two paths spill).
+__device__ __noinline__ float far_block(uint32_t tb, float a, float w) {
+  float m = a * w, f = 1.f, g = 1.f;
+  if (fabsf(m) < FLT_MIN) {
+    const bool less = fabsf(a) < fabsf(w);  // the smaller is below 2^-63, or one is zero
+    m = (less ? a : w) * 0x1p64f * (less ? w : a);
+    f = 0x1p-64f;
+  } else if (!(fabsf(m) <= FLT_MAX)) {
+    m = a * 0x1p-64f * (w * 0x1p-64f);
+    f = g = 0x1p64f;
   }
-  return make_float2(a * 0x1p-64f * (w * 0x1p-64f), 0x1p64f);  // the sums' factor twice
-}
-// r times what far_scales left to the sums.
-__device__ __forceinline__ void scale32(uint32_t* r, float f) {
-  const float g = f > 1.f ? f : 1.f;
+#pragma unroll 1
+  for (int i = 0; i < 64; i += 8) {
+    float r[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+          "=f"(r[7])
+        : "r"(tb + i)
+        : "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f * g);
+    for (int j = 0; j < 8; ++j) r[j] = r[j] * f * g;
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(tb + i),
+        "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+        : "memory");
+  }
+  return m;
 }
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   float4 v;
@@ -555,40 +575,36 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                           ((int64_t)t.e * p.n_blocks + b1) * p.k_blocks;
         const float* as = p.a_scale + (int64_t)t.row0 * p.k_blocks;
         for (int kb = kb0; kb < kb1; kb += GROUP) {
-          float v[4][GROUP], w = 0.f;
+          float v[4][GROUP], w = 1.f;  // 1 where there is none
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int k = 0; k < GROUP; ++k) {
               const int r = 32 * i + lane;
               v[i][k] = r < t.valid && kb + k < kb1 ? __ldg(as + (int64_t)r * p.k_blocks + kb + k)
-                                                    : 0.f;
+                                                    : 1.f;
             }
           if (lane < 2 * GROUP && kb + (lane >> 1) < kb1)
             w = __ldg((lane & 1 ? w1 : w0) + kb + (lane >> 1));
           ok = wait_ctrl(sempty_bar(slot), phase ^ 1u);
           if (!ok) break;
           ScaleSlot& s = slots[slot];
-          // lane k of the first GROUP keeps whether block k has products far out
-          bool far = false;
+          // Zeros and negative scales are taken for far ones, and handled as what they
+          // are; a NaN is passed over, and gives NaN either way.
+          float lo = w, hi = w;
 #pragma unroll
-          for (int k = 0; k < GROUP; ++k) {
-            const float wa = __shfl_sync(0xffffffffu, w, 2 * k);
-            const float wb = __shfl_sync(0xffffffffu, w, 2 * k + 1);
-            bool out = false;
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int k = 0; k < GROUP; ++k) {
               s.a[k][32 * i + lane] = v[i][k];
-              out |= 32 * i + lane < t.valid &&
-                     !(scales_fit(v[i][k], wa) && scales_fit(v[i][k], wb));
+              lo = fminf(lo, v[i][k]);
+              hi = fmaxf(hi, v[i][k]);
             }
-            out = __any_sync(0xffffffffu, out);
-            if (lane == k) far = out;
-          }
-          if (lane < 2 * GROUP) reinterpret_cast<float*>(&s.w[lane >> 1])[lane & 1] = w;
-          if (lane < GROUP) s.w[lane].z = far ? 1.f : 0.f;
+          if (lane < 2 * GROUP) reinterpret_cast<float*>(s.w)[lane] = w;
+          const bool far = __any_sync(0xffffffffu, lo < NEAR_LO || hi > NEAR_HI);
           if (lane == 0) {
             s.e = t.e; s.nb = t.nb; s.row0 = t.row0; s.valid = t.valid;
+            s.far[0] = far;
           }
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(sfull_bar(slot));
@@ -604,7 +620,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint8_t* stage = staging + (warp - FIRST_EPI_WARP) * 2048;
     uint32_t acc = 0, acc_phase = 0, mphase = 0, sphase = 0;
     int slot = 0;
-    bool ok = true, ready = false, sready = false;
+    bool ok = true, ready = false, sready = false, far = false;
     for (int tile = first; tile < total; tile += step) {
       float c[128];
 #pragma unroll
@@ -614,12 +630,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int kb = kb0; kb < kb1; ++kb) {
         const int k = (kb - kb0) & (GROUP - 1);
         // Both barriers of this block were tested before the last block's sums
-        // were added; only one that had not completed is waited for.
+        // were added; only one that had not completed is waited for. So was `far`
+        // read, the group's flag.
         if (k == 0) {
           if (!__all_sync(0xffffffffu, sready)) {
             ok = wait_inline(sfull_bar(slot), sphase, abort_flag, tmo);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
+            far = slots[slot].far[0] != 0;
           }
           if (kb == kb0) {
             t.e = slots[slot].e; t.nb = slots[slot].nb;
@@ -627,21 +645,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             work = quad * 32 < t.valid;
           }
         }
-        const float sa = slots[slot].a[k][r_in_tile];
-        const float4 sw = slots[slot].w[k];
-        float m0 = sa * sw.x, m1 = sa * sw.y, f0 = 1.f, f1 = 1.f;
-        const bool far = sw.z != 0.f;  // warp-uniform, and rare
-        if (far) {
-          const float2 q0 = far_scales(sa, sw.x), q1 = far_scales(sa, sw.y);
-          m0 = q0.x; f0 = q0.y; m1 = q1.x; f1 = q1.y;
-        }
-        if (!__all_sync(0xffffffffu, ready)) {
+        float sa = slots[slot].a[k][r_in_tile];
+        float2 sw = slots[slot].w[k];
+        const uint32_t tb =
+            tmem_base + acc * BN + half * 64 + (static_cast<uint32_t>(quad * 32) << 16);
+        if (!__all_sync(0xffffffffu, ready && !far)) {
           ok = wait_inline(tfull_bar(acc), acc_phase, abort_flag, tmo);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
+          if (far && work) {  // in a branch that is there for the wait
+            tc::tc_fence_after();
+            sw.x = far_block(tb, sa, sw.x);
+            sw.y = far_block(tb + 128, sa, sw.y);
+            sa = 1.f;
+          }
         }
-        const uint32_t tb =
-            tmem_base + acc * BN + half * 64 + (static_cast<uint32_t>(quad * 32) << 16);
         uint32_t r0[32], r1[32];
         if (work) {
           tc::tc_fence_after();
@@ -652,10 +670,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ld32(tb + 32, r1);
           wait_ld(r0);
           pass_regs(r1);
-          if (far) { scale32(r0, f0); scale32(r1, f0); }
-          promote32(c, r0, m0);
+          promote32(c, r0, sa * sw.x);
           ld32(tb + 128, r0);
-          promote32(c + 32, r1, m0);
+          promote32(c + 32, r1, sa * sw.x);
           ld32(tb + 160, r1);
           wait_ld(r0);
           pass_regs(r1);
@@ -669,12 +686,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (lane == 0) tc::mbar_arrive(sempty_bar(slot));
           if (++slot == SCALE_SLOTS) { slot = 0; sphase ^= 1u; }
           sready = mbar_test(sfull_bar(slot), sphase);
+          if (sready) far = slots[slot].far[0] != 0;
         }
         ready = mbar_test(tfull_bar(acc), acc_phase);
         if (work) {
-          if (far) { scale32(r0, f1); scale32(r1, f1); }
-          promote32(c + 64, r0, m1);
-          promote32(c + 96, r1, m1);
+          promote32(c + 64, r0, sa * sw.y);
+          promote32(c + 96, r1, sa * sw.y);
         }
       }
       if (!ok) break;

@@ -634,3 +634,30 @@ def test_empty_matrices():
                 dequantize_fp8_block(empty(rows, cols, dtype=torch.uint8),
                                      empty(rows if block_rows == 1 else ceil(rows, 128), ceil(cols, 128)),
                                      block_rows)
+
+
+@pytest.mark.parametrize("M,N,K,E", [(3, 1200, 2304, 0), (3000, 2100, 2304, 0), (900, 272, 1296, 5)])
+def test_a_few_blocks_of_far_scales(M, N, K, E):
+    # two K blocks far apart, each out of range one way, among ordinary ones; some
+    # rows and weight blocks are ordinary there too; a zero and a negative scale
+    a, sa, w, sw = operands(M, N, K, E, seed=95)
+    kb = ceil(K, BLK)
+    lo, hi = kb // 2 - 1, kb - 1
+    sa[::2, lo] *= 2.0 ** -110
+    sw[..., lo] *= 2.0 ** -20
+    sa[:, hi] *= 2.0 ** 90
+    sw[..., hi] *= 2.0 ** 50
+    a[:, hi * BLK:] = 0                           # a product of 2^140, of sums that are zero
+    sa[1, 0] = 0.0
+    sa[2, 1] *= -1.0
+    offsets = cuts = None
+    if E:
+        cuts = [0, 200, 200, 201, 650, M]
+        offsets = torch.tensor(cuts, dtype=torch.int32, device="cuda")
+    want, mag = product(a, sa, w, sw, cuts)
+    near(matmul_fp8_block(a, sa, w, sw, offsets=offsets, out_dtype=torch.float32), want, mag, K)
+    if N % 16 == 0:
+        u = w.flip(0).contiguous()
+        codes, scales = swiglu_fp8_block(a, sa, w, u, sw, sw, offsets=offsets)
+        check_swiglu(codes, scales, *swiglu_reference(a, sa, w, sw, u, sw, cuts))
+    assert moe_get_device_status() == 0
