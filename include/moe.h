@@ -478,7 +478,7 @@ typedef struct {
   void* stream;
 } moe_balance_dims;
 
-#define MOE_BALANCE_SMALL_T 32 /* tokens that one thread block takes */
+#define MOE_BALANCE_SMALL_T 32 /* tokens that one thread block takes at least */
 
 MOE_API size_t moe_balance_loss_workspace_size(const moe_balance_dims* dims);
 

@@ -149,7 +149,9 @@ def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, gate_mode: int = 
 
     logits [T, E] fp32 or bf16, rows may be strided: what the softmax of the layer
     sees. After `forward`, routing_views(...)["logits"] and ["topk_idx"] are
-    these arguments (add router_bias to the logits if the layer has one).
+    these arguments (add router_bias to the logits if the layer has one). The views
+    carry no graph: a trainer whose gradient is to reach W_r and x computes the
+    logits by itself (x.float() @ W_r.t()), or chains balance_loss_backward's result.
     topk_idx int32 [T, k]: the chosen experts; entries outside [0, E), like -1 for
     a dropped slot, count for none.
     gate_mode: as in forward (2: the probabilities are normalised sigmoids).

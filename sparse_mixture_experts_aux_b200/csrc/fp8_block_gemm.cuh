@@ -32,14 +32,18 @@
 // some builds and not in others (4736 x 4096 x 8192: 157 to 242 us by chance).
 //
 // Bound. Many rows: the way round between the MMAs of a block (512 cycles) and
-// the epilogue's reads of it, about 860 cycles a block with the tensor pipe 53%
-// active: 4736 x 4096 x 8192 in 134 to 150 us (2.1 to 2.4 PFLOP/s) from a cool
-// start; back to back the power cap sets 1.6 to 1.7 PFLOP/s (8 experts' gate and
-// up over 8192 rows, 4096 -> 14336: 1180 us). Few rows: HBM; the same experts
-// over 64 rows 160 us in the layer, 5.9 TB/s, 0.90 of the measured copy. Not
-// kept, as slower: CTA pairs (tcgen05 cta_group::2; 171 us where this form takes
-// 150), four TMEM buffers of 128 columns (173), loading a block's first columns
+// the epilogue's reads of it, about 960 cycles a block with the tensor pipe 53%
+// active: 4736 x 4096 x 8192 in 151 to 160 us as a single call (2.0 to 2.1
+// PFLOP/s), 177 us back to back (1.8), when the power cap holds the clock at 1.5
+// GHz. A library product without block scales runs into the same cap and makes 2.15
+// PFLOP/s of it (147 us): the cycles are this kernel's own. 8 experts' gate and up
+// over 8192 rows, 4096 -> 14336: 1240 us back to back. Few rows: HBM; the same
+// experts over 64 rows 166 us in the layer, 5.7 TB/s, 0.86 of the measured copy.
+// Not kept, as slower: CTA pairs (tcgen05 cta_group::2; 171 us where this form then
+// took 150), four TMEM buffers of 128 columns (173), loading a block's first columns
 // while the last block is added (169), a deeper ring for few rows (181 -> 189 us).
+// The K loop's code is sensitive: the same source compiled in parallel pieces (nvcc
+// -split-compile) varied by 10%; these figures are of the library's own build.
 //
 // Tiles of 128 rows never straddle two experts; rows of a tile behind its
 // expert's last row are computed from whatever lies there and not stored (a
@@ -213,7 +217,8 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
 // role has given up or timeout_ns have passed (recorded, and the abort flag
 // raised). In line, unlike
 // the one in tc_gemm.cuh: the epilogue warps wait with 128 accumulators in
-// registers, which a call would spill. The first test does not suspend the warp and
+// registers. (What spills is the adding loop of MATMUL with SPLIT, 128 bytes a
+// thread for its 64 sums in flight.) The first test does not suspend the warp and
 // the limit is checked before the next, so that a limit of nothing ends the
 // first wait that is not over.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {

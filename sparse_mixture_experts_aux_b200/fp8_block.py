@@ -33,7 +33,7 @@ def quantize_fp8_block(w: torch.Tensor, block_rows: int = 128, stream=None):
     block_rows = 1 (activations): w [..., cols], scales [..., ceil(cols / 128)];
     the rows of a 2-D w may be strided. block_rows = 128 (weights): w [..., rows,
     cols], scales [..., ceil(rows / 128), ceil(cols / 128)]. bf16 or fp32, cols a
-    multiple of 16.
+    multiple of 16. No gradient: the results of a w that requires one do not.
     """
     if not w.is_cuda:
         raise RuntimeError("w must be a CUDA tensor (there is no CPU path)")
@@ -61,7 +61,8 @@ def quantize_fp8_block(w: torch.Tensor, block_rows: int = 128, stream=None):
 
 def dequantize_fp8_block(codes: torch.Tensor, scales: torch.Tensor, block_rows: int = 128,
                          stream=None) -> torch.Tensor:
-    """fp32 values code * scale of quantize_fp8_block's results (moe_dequantize_fp8_block)."""
+    """fp32 values code * scale of quantize_fp8_block's results
+    (moe_dequantize_fp8_block). No gradient."""
     if not codes.is_cuda or not codes.is_contiguous() or codes.dim() < 2 or codes.dtype not in _CODES:
         raise RuntimeError("codes must be a contiguous CUDA tensor of E4M3 codes with rows and columns")
     rows, cols = codes.shape[-2:]

@@ -18,7 +18,8 @@ def dtype_code(dt: torch.dtype) -> int:
 
 
 class Workspace:
-    """A reusable device scratch buffer (torch-allocated, 512-byte aligned)."""
+    """A reusable device scratch buffer (torch-allocated, 512-byte aligned). A larger
+    request replaces the buffer: one that a captured graph runs in must not get one."""
 
     def __init__(self, device=None):
         self.buf: Optional[torch.Tensor] = None

@@ -422,7 +422,11 @@ def test_long_batch_sums_stay_exact():
 def test_rows_far_from_zero(E, gate_mode, dtype):
     # finite rows whose largest logit is far from zero, up to the type's last value:
     # r - max rounds by half an ulp of itself whatever max is, so eps_p holds with R
-    # the differences that still count (e^-100 of the largest term is zero in fp32)
+    # the differences that still count (e^-100 of the largest term is zero in fp32).
+    # In the kernel's own operations: r - max and its product with log2 e round once
+    # each, log2 e itself is off by 0.22 2^-24, in all 1.11 |r - max| 2^-23; what is
+    # above R 2^-23 (below 10 2^-23 where the term is not zero), two ulp of 2^x, one of
+    # the reciprocal and the products' halves fit into the 16 2^-23
     top = torch.finfo(dtype).max
     far = [s * v for v in (1e4, 1e9, 1e10, 1e12, 1e30, top) for s in (1.0, -1.0)]
     logits, idx = draw(4 * len(far), E, 2, dtype, seed=17)
