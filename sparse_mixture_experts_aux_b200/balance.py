@@ -159,7 +159,8 @@ def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, gate_mode: int = 
     cu_seqlens int32 [S + 1]: sequence s is tokens cu[s] .. cu[s + 1] - 1.
     stream: where to run instead of the current stream (not with a gradient: use
     torch.cuda.stream). The inputs must be ready there, and the results are: wait
-    for it before they are used elsewhere. Both may be dropped at any time.
+    for it before they are used elsewhere. Both may be dropped at any time; a raw
+    cudaStream_t has to outlive them.
     """
     _no_tangent("balance_loss", logits)
     if torch.is_grad_enabled() and logits.requires_grad:

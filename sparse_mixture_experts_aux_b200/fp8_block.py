@@ -3,7 +3,7 @@ moe_*_fp8_block): argument checks and marshalling; the library computes.
 
 stream= in each of them: where to run instead of the current stream. The inputs
 must be ready there, and the results are: wait for it before they are used
-elsewhere. Both may be dropped at any time."""
+elsewhere. Both may be dropped at any time; a raw cudaStream_t has to outlive them."""
 from __future__ import annotations
 
 import math

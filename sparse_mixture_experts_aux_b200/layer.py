@@ -82,7 +82,7 @@ def forward(x: torch.Tensor, W_r: torch.Tensor, W_g: torch.Tensor, W_u: torch.Te
     scale for each 128 columns inside the experts.
     stream: where to run instead of the current stream. The inputs must be ready
     there, and the results are: wait for it before they are used elsewhere. Both may
-    be dropped at any time.
+    be dropped at any time; a raw cudaStream_t has to outlive them.
     wait_timeout_ns: limit of the GEMM kernels' device-side waits (0 = library default).
     gate_mode / selection_bias / n_group / topk_group: routing variants (include/moe.h).
     """

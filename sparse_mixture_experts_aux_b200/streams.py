@@ -3,7 +3,9 @@
 torch's allocator hands a freed block out again in the order of the stream that
 it was allocated on. A call that runs on another stream than the current one
 therefore allocates on that other stream, lends it the caller's tensors, and
-gives its results to the current stream.
+gives its results to the current stream. A stream given as a raw cudaStream_t has
+to exist, as torch.cuda.ExternalStream asks, until the tensors of its calls are
+dropped: torch records an event on it then.
 """
 from __future__ import annotations
 
